@@ -36,7 +36,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 RA_OK, RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_WORKSPACE = 0, 1, 2, 3
 RA_ERR_CUDA, RA_ERR_TIMEOUT, RA_ERR_DEVICE_BOUNDS = 4, 5, 6
-RA_F32, RA_BF16 = 0, 1
+RA_F32, RA_BF16, RA_I8, RA_E4M3 = 0, 1, 2, 3
 RA_PART_CONTIGUOUS, RA_PART_ZIGZAG = 0, 1
 RA_ORDER_RING, RA_ORDER_TOKENRING = 0, 1
 RA_SCHED_AUTO, RA_SCHED_UNFUSED, RA_SCHED_EPILOGUE_FUSED, RA_SCHED_PERSISTENT = 0, 1, 2, 3
@@ -51,7 +51,7 @@ EXPORTED = ["ra_block_attn", "ra_block_attn_merge", "ra_merge_partial", "ra_merg
             "ra_status_string", "ra_version", "ra_ring_attention_noalloc", "ra_noalloc_scratch_bytes",
             "ra_decode_attention", "ra_decode_workspace", "ra_decode_splits", "ra_ring_attention_backward",
             "ra_ring_attention_backward_workspace", "ra_debug_build", "ra_get_bounds_record",
-            "ra_set_cta_timeline"]
+            "ra_set_cta_timeline", "ra_cache_append", "ra_cache_read"]
 
 RA_TIMELINE_ATTN_FWD, RA_TIMELINE_BWD_DKV, RA_TIMELINE_BWD_DQ = 0, 1, 2
 TIMELINE_KERNELS = {"attn_fwd": RA_TIMELINE_ATTN_FWD, "bwd_dkv": RA_TIMELINE_BWD_DKV, "bwd_dq": RA_TIMELINE_BWD_DQ}
@@ -60,6 +60,14 @@ TIMELINE_KERNELS = {"attn_fwd": RA_TIMELINE_ATTN_FWD, "bwd_dkv": RA_TIMELINE_BWD
 class ra_options(ctypes.Structure):
     _fields_ = [("order", ctypes.c_int), ("sched", ctypes.c_int), ("attn_event_begin", ctypes.c_void_p),
                 ("attn_event_end", ctypes.c_void_p), ("tiling", ctypes.c_int), ("fault_inject", ctypes.c_int)]
+
+
+class ra_paged_cache(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("key_bounds", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+                ("page_table", ctypes.c_void_p), ("B", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("seq_lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p)]
 
 
 TILINGS = {"auto": 0, "row_pairs": 1, "kv_split": 2, "cluster2": 3}
@@ -109,6 +117,10 @@ _lib.ra_get_bounds_record.argtypes = [ctypes.POINTER(ctypes.c_int64)]
 _lib.ra_get_bounds_record.restype = _i
 _lib.ra_set_cta_timeline.argtypes = [_vp, _i64, _i]
 _lib.ra_set_cta_timeline.restype = _i
+_lib.ra_cache_append.argtypes = [ctypes.POINTER(ra_paged_cache), _vp, _vp, _i, _i, _vp]
+_lib.ra_cache_append.restype = _i
+_lib.ra_cache_read.argtypes = [ctypes.POINTER(ra_paged_cache), _i, _i, _vp, _vp, _i, _vp]
+_lib.ra_cache_read.restype = _i
 
 
 class RAError(RuntimeError):
@@ -415,3 +427,90 @@ def ra_decode_attention(q, k, v, causal: bool = True, n_splits: int = 0, out=Non
                                     _stream(stream)), "ra_decode_attention")
     return out, lse
 
+
+# ------------------------------------------------------- paged key-value cache
+# Pages [n_pages, Hkv, page_size, D] (bf16, int8 or float8_e4m3fn), scales fp32
+# [n_pages, Hkv, page_size] for an 8-bit cache, key_bounds bf16
+# [n_pages, Hkv, 2, D]; page_table int32 [B, max_pages], seq_lens and new_lens
+# int32 [B] on the device: see ra_paged_cache in include/ra.h.
+
+_CACHE_DTYPES = {torch.bfloat16: RA_BF16, torch.int8: RA_I8, torch.float8_e4m3fn: RA_E4M3}
+
+
+def _expect(t: torch.Tensor | None, name: str, dtype, shape, device) -> int | None:
+    """The address of t, checked: contiguous, on `device`, of this dtype and shape."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _paged(k_pages, v_pages, k_scales, v_scales, key_bounds, page_table, seq_lens, new_lens) -> ra_paged_cache:
+    """The C argument of a cache and its batch (shapes and devices checked)."""
+    dev = k_pages.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be contiguous CUDA tensors")
+    if k_pages.dim() != 4 or k_pages.dtype not in _CACHE_DTYPES:
+        raise ValueError("k_pages must be [n_pages, Hkv, page_size, D] in bfloat16, int8 or float8_e4m3fn")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    n_pages, Hkv, page_size, D = k_pages.shape
+    B, max_pages = page_table.shape
+    code = _CACHE_DTYPES[k_pages.dtype]
+    if (code == RA_BF16) != (k_scales is None) or (code == RA_BF16) != (v_scales is None):
+        raise ValueError("an 8-bit cache has k_scales and v_scales, a bfloat16 one has none")
+    f32, i32 = torch.float32, torch.int32
+    rows = (n_pages, Hkv, page_size)
+    return ra_paged_cache(
+        _expect(k_pages, "k_pages", k_pages.dtype, k_pages.shape, dev),
+        _expect(v_pages, "v_pages", k_pages.dtype, k_pages.shape, dev),
+        _expect(k_scales, "k_scales", f32, rows, dev), _expect(v_scales, "v_scales", f32, rows, dev),
+        _expect(key_bounds, "key_bounds", torch.bfloat16, (n_pages, Hkv, 2, D), dev), code, n_pages, page_size, Hkv, D,
+        _expect(page_table, "page_table", i32, page_table.shape, dev), B, max_pages,
+        _expect(seq_lens, "seq_lens", i32, (B,), dev), _expect(new_lens, "new_lens", i32, (B,), dev))
+
+
+def _call_on(dev: torch.device, stream, fn, what: str, *args) -> None:
+    """fn(*args, stream) with `dev` current, on the given stream or on dev's
+    current one (not another device's)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)), what)
+    else:
+        _check(fn(*args, _stream(stream)), what)
+
+
+def ra_cache_append(k, v, k_pages, v_pages, page_table, seq_lens, new_lens=None, k_scales=None, v_scales=None,
+                    key_bounds=None, stream=None) -> None:
+    """Writes the new tokens k, v [B, T, Hkv, D] (bf16) into the pages, with the
+    scales of an 8-bit cache and, if given, the pages' key bounds.  seq_lens
+    counts the new tokens in; row i < new_lens[b] is the token at position
+    seq_lens[b] - new_lens[b] + i (None: min(T, seq_lens[b]) of them)."""
+    c = _paged(k_pages, v_pages, k_scales, v_scales, key_bounds, page_table, seq_lens, new_lens)
+    if k.dim() != 4:
+        raise ValueError("k must be [B, T, Hkv, D]")
+    T = k.shape[1]
+    shape, dev = (c.B, T, c.Hkv, c.D), k_pages.device
+    _call_on(dev, stream, _lib.ra_cache_append, "ra_cache_append", ctypes.byref(c),
+             _expect(k, "k", k.dtype, shape, dev), _expect(v, "v", k.dtype, shape, dev), _dtype_code(k.dtype), T)
+
+
+def ra_cache_read(k_pages, v_pages, page_table, seq_lens, T: int, first: int = 0, k_scales=None, v_scales=None,
+                  k=None, v=None, out_dtype=None, stream=None):
+    """Tokens first .. first + T - 1 of every sequence as dense (k, v)
+    [B, T, Hkv, D], zero at and behind seq_lens[b]; out_dtype bfloat16 (default)
+    or float32."""
+    c = _paged(k_pages, v_pages, k_scales, v_scales, None, page_table, seq_lens, None)
+    shape, dev = (c.B, T, c.Hkv, c.D), k_pages.device
+    odt = out_dtype or (k.dtype if k is not None else v.dtype if v is not None else torch.bfloat16)
+    if k is None:
+        k = torch.empty(shape, dtype=odt, device=dev)
+    if v is None:
+        v = torch.empty(shape, dtype=odt, device=dev)
+    _call_on(dev, stream, _lib.ra_cache_read, "ra_cache_read", ctypes.byref(c), first, T,
+             _expect(k, "k", odt, shape, dev), _expect(v, "v", odt, shape, dev), _dtype_code(odt))
+    return k, v

@@ -1036,3 +1036,5 @@ ra_status ra_ring_attention_backward(const void* q, const void* k, const void* v
 }
 
 }  // extern "C"
+
+#include "paged_api.cuh"

@@ -52,7 +52,9 @@ typedef enum {
   RA_ERR_DEVICE_BOUNDS = 6  /* device: an index check failed (access skipped)    */
 } ra_status;
 
-typedef enum { RA_F32 = 0, RA_BF16 = 1 } ra_dtype;
+/* RA_I8 (signed 8-bit codes) and RA_E4M3 (8-bit floats, 4 exponent and 3
+ * mantissa bits) are types of a paged cache's keys and values only. */
+typedef enum { RA_F32 = 0, RA_BF16 = 1, RA_I8 = 2, RA_E4M3 = 3 } ra_dtype;
 
 /* [TR] "If this is right" (zigzag) and "Referee Report, Summary" (contiguous).
  * Contiguous: block r = tokens [r*L, (r+1)*L), L = S / n_blocks.
@@ -302,6 +304,83 @@ size_t ra_decode_workspace(int B, int Tq, int Skv, int Hq, int Hkv, int D, int n
 
 /* Chunks ra_decode_attention uses for these arguments (-1 when invalid). */
 int ra_decode_splits(int B, int Tq, int Skv, int Hq, int Hkv, int D, int n_splits);
+
+/*
+ * A paged key-value cache and the batch that uses it: the argument of the
+ * ra_cache_*, ra_paged_decode_* and ra_page_select_* calls.  [TR] "Reading
+ * between the lines": the decode phase as KV-cache chunking; here a chunk is a
+ * page that may lie anywhere in memory, and the page table gives its place.
+ * (The pages on the method have no cache layout: this one is the library's.)
+ *
+ *  k_pages, v_pages  device, `dtype` (RA_BF16, RA_I8 or RA_E4M3), [n_pages, Hkv,
+ *             page_size, D]: the rows of one KV head of one page are adjacent.
+ *  k_scales, v_scales  device fp32 [n_pages, Hkv, page_size]: one scale for
+ *             each row of an 8-bit cache (value = code * scale); NULL for RA_BF16.
+ *  key_bounds  device bf16 [n_pages, Hkv, 2, D]: for each column the smallest
+ *             and the largest key of the page.  NULL where a call does not use it.
+ *  dtype, n_pages, page_size, Hkv, D   page_size in {16, 32, 64, 128}; D in
+ *             {64, 128}; n_pages * Hkv * page_size < 2^31 - 128.
+ *  page_table  device int32 [B, max_pages]: page of tokens [i page_size,
+ *             (i + 1) page_size) of a sequence.  Entries behind a sequence's
+ *             last token are not read.
+ *  B, max_pages  sequences; table entries of each (max_pages * page_size < 2^31).
+ *  seq_lens   device int32 [B]: tokens of each sequence in the cache, the new
+ *             ones of this step included; 0 for an empty slot.
+ *  new_lens   device int32 [B], 0 <= new_lens[b] <= min(T, seq_lens[b]): how
+ *             many of the T token rows given for sequence b are real.  Row
+ *             i < new_lens[b] is the token at position seq_lens[b] -
+ *             new_lens[b] + i.  NULL: min(T, seq_lens[b]).
+ * Device integers are checked on the device: a length outside its range or a
+ * page outside [0, n_pages) is recorded as RA_ERR_DEVICE_BOUNDS in the device
+ * status word, in the release build too; nothing outside the buffers is
+ * accessed, and what the call writes for that sequence is undefined.
+ * Pages, scales and bounds must be 16-byte aligned, the int32 arrays 4-byte.
+ */
+typedef struct {
+  void* k_pages;
+  void* v_pages;
+  float* k_scales;
+  float* v_scales;
+  void* key_bounds;
+  ra_dtype dtype;
+  int n_pages, page_size, Hkv, D;
+  const int32_t* page_table;
+  int B, max_pages;
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+} ra_paged_cache;
+
+/*
+ * ra_cache_append - writes the new tokens' keys and values into the cache.
+ *  cache      as above; k_pages, v_pages (and scales, bounds) are written.  The
+ *             page table and lengths are those after the step.
+ *  k, v       device, bf16, [B, T, Hkv, D]; in_dtype must be RA_BF16.  Rows
+ *             i >= new_lens[b] are not read.
+ * RA_BF16 pages take the rows as they are.  An 8-bit row x gets the scale
+ *     s = fp32(max |x| / m),  m = 127 (RA_I8) or 448 (RA_E4M3)
+ * and the codes x / s, each the nearest value of the type to the exact quotient,
+ * ties to the even one.  A row with max |x| < 2^-100 gets scale and codes 0; a
+ * row that holds a NaN or an infinity gets the scale NaN and codes 0.
+ * key_bounds, if given, are those of the bf16 keys before they are rounded to
+ * 8 bits, NaN ignored: a page whose first row is written starts anew, another
+ * page's bounds are widened.  Each page is written by one sequence: two
+ * sequences that share a page may both read it, but must not append to it.
+ * No atomics: the result does not depend on scheduling.
+ */
+ra_status ra_cache_append(const ra_paged_cache* cache, const void* k, const void* v, ra_dtype in_dtype, int T,
+                          void* stream);
+
+/*
+ * ra_cache_read - tokens first .. first + T - 1 of every sequence as dense
+ * keys and values (for ra_ring_attention over a cached prefix).
+ *  first >= 0, T >= 1; cache->new_lens and key_bounds are not used.
+ *  k, v       device, out_dtype (RA_F32 or RA_BF16), [B, T, Hkv, D]; either may
+ *             be NULL.  Values of an 8-bit cache are code * scale in fp32,
+ *             rounded once more (nearest even) for RA_BF16.  Rows at or behind
+ *             seq_lens[b] are written as zeros.
+ */
+ra_status ra_cache_read(const ra_paged_cache* cache, int first, int T, void* k, void* v, ra_dtype out_dtype,
+                        void* stream);
 
 /*
  * ra_ring_attention_backward - gradients of ra_ring_attention.
