@@ -51,7 +51,8 @@ EXPORTED = ["ra_block_attn", "ra_block_attn_merge", "ra_merge_partial", "ra_merg
             "ra_status_string", "ra_version", "ra_ring_attention_noalloc", "ra_noalloc_scratch_bytes",
             "ra_decode_attention", "ra_decode_workspace", "ra_decode_splits", "ra_ring_attention_backward",
             "ra_ring_attention_backward_workspace", "ra_debug_build", "ra_get_bounds_record",
-            "ra_set_cta_timeline", "ra_cache_append", "ra_cache_read"]
+            "ra_set_cta_timeline", "ra_cache_append", "ra_cache_read",
+            "ra_paged_decode_attention", "ra_paged_decode_workspace"]
 
 RA_TIMELINE_ATTN_FWD, RA_TIMELINE_BWD_DKV, RA_TIMELINE_BWD_DQ = 0, 1, 2
 TIMELINE_KERNELS = {"attn_fwd": RA_TIMELINE_ATTN_FWD, "bwd_dkv": RA_TIMELINE_BWD_DKV, "bwd_dq": RA_TIMELINE_BWD_DQ}
@@ -121,6 +122,11 @@ _lib.ra_cache_append.argtypes = [ctypes.POINTER(ra_paged_cache), _vp, _vp, _i, _
 _lib.ra_cache_append.restype = _i
 _lib.ra_cache_read.argtypes = [ctypes.POINTER(ra_paged_cache), _i, _i, _vp, _vp, _i, _vp]
 _lib.ra_cache_read.restype = _i
+_lib.ra_paged_decode_attention.argtypes = [_vp, _i, ctypes.POINTER(ra_paged_cache), _i, _i, _i, _vp, _i, _vp, _i, _vp,
+                                           _vp, _sz, _vp]
+_lib.ra_paged_decode_attention.restype = _i
+_lib.ra_paged_decode_workspace.argtypes = [_i, _i, _i, _i, _i]
+_lib.ra_paged_decode_workspace.restype = _sz
 
 
 class RAError(RuntimeError):
@@ -514,3 +520,43 @@ def ra_cache_read(k_pages, v_pages, page_table, seq_lens, T: int, first: int = 0
     _call_on(dev, stream, _lib.ra_cache_read, "ra_cache_read", ctypes.byref(c), first, T,
              _expect(k, "k", odt, shape, dev), _expect(v, "v", odt, shape, dev), _dtype_code(odt))
     return k, v
+
+
+def ra_paged_decode_workspace(B, Tq, Hq, Hkv, D) -> int:
+    n = _lib.ra_paged_decode_workspace(B, Tq, Hq, Hkv, D)
+    if n == ctypes.c_size_t(-1).value:
+        raise RAError(RA_ERR_INVALID_ARG, "ra_paged_decode_workspace")
+    return n
+
+
+def ra_paged_decode_attention(q, k_pages, v_pages, page_table, seq_lens, new_lens=None, k_scales=None, v_scales=None,
+                              causal: bool = True, selected=None, out=None, lse=None, out_dtype=None, workspace=None,
+                              stream=None):
+    """Attention of the new tokens' queries q [B, Tq, Hq, D] (bf16) over the paged
+    cache, or over the pages selected [B, Hkv, n_sel] (int32, as ra_page_select
+    gives them).  Row i < new_lens[b] is the token at position seq_lens[b] -
+    new_lens[b] + i (None: min(Tq, seq_lens[b]) real rows).  Returns
+    (out [B, Tq, Hq, D] in out_dtype, default float32; lse [B, Tq, Hq] float32)."""
+    c = _paged(k_pages, v_pages, k_scales, v_scales, None, page_table, seq_lens, new_lens)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Tq, Hq, D]")
+    _, Tq, Hq, _ = q.shape
+    shape, dev = (c.B, Tq, Hq, c.D), k_pages.device
+    odt = out_dtype or (out.dtype if out is not None else torch.float32)
+    if out is None:
+        out = torch.empty(shape, dtype=odt, device=dev)
+    if lse is None:
+        lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
+    n_sel = 0
+    if selected is not None:
+        if selected.dim() != 3:
+            raise ValueError("selected must be [B, Hkv, n_sel]")
+        n_sel = selected.shape[2]
+    if workspace is None:
+        workspace = torch.empty(ra_paged_decode_workspace(c.B, Tq, Hq, c.Hkv, c.D), dtype=torch.uint8, device=dev)
+    _call_on(dev, stream, _lib.ra_paged_decode_attention, "ra_paged_decode_attention", _expect(q, "q", q.dtype, shape, dev),
+             _dtype_code(q.dtype), ctypes.byref(c), Tq, Hq, int(bool(causal)),
+             _expect(selected, "selected", torch.int32, (c.B, c.Hkv, n_sel), dev), n_sel,
+             _expect(out, "out", odt, shape, dev), _dtype_code(odt), _expect(lse, "lse", torch.float32, shape[:3], dev),
+             _ptr(workspace), workspace.numel() * workspace.element_size())
+    return out, lse

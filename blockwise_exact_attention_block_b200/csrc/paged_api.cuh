@@ -3,6 +3,7 @@
 #pragma once
 
 #include "paged.cuh"
+#include "paged_decode.cuh"
 
 namespace {
 
@@ -22,7 +23,7 @@ ra_status check_batch(const ra_paged_cache* c) {
   if (c->B < 1 || c->max_pages < 1 || c->n_pages < 1 || c->Hkv < 1) return RA_ERR_INVALID_ARG;
   if (page_shift_of(c->page_size) < 0 || (c->D != 64 && c->D != 128)) return RA_ERR_UNSUPPORTED;
   if (static_cast<long long>(c->n_pages) * c->Hkv * c->page_size >= 0x7fffffffLL - 127) return RA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(c->max_pages) * c->page_size >= 0x7fffffffLL) return RA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(c->max_pages) * c->page_size > kPgNone) return RA_ERR_UNSUPPORTED;  // see kPgNone
   if (!c->page_table || !c->seq_lens) return RA_ERR_INVALID_ARG;
   if (!aligned4(c->page_table) || !aligned4(c->seq_lens) || !aligned4(c->new_lens)) return RA_ERR_INVALID_ARG;
   return RA_OK;
@@ -69,6 +70,103 @@ ra_status launch_read_t(const ReadArgs& a, int et, unsigned grid, cudaStream_t s
   else if (et == kCacheI8) cache_read_kernel<D, kCacheI8, Tout><<<grid, 256, 0, st>>>(a);
   else cache_read_kernel<D, kCacheE4M3, Tout><<<grid, 256, 0, st>>>(a);
   return cuda_status(cudaGetLastError());
+}
+
+// Pages of one tensor as rows of D values, box = 16 or 32 rows of one column
+// half (128 bytes; whole rows of an 8-bit cache), swizzled for the fragment loads.
+bool make_page_map(CUtensorMap* m, const void* ptr, const ra_paged_cache* c) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const int elem = c->dtype == RA_BF16 ? 2 : 1;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c->D),
+                              static_cast<cuuint64_t>(c->n_pages) * c->Hkv * c->page_size};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(c->D) * elem};
+  const cuuint32_t cols = static_cast<cuuint32_t>(c->D * elem > 128 ? 128 / elem : c->D);
+  const cuuint32_t box[2] = {cols, c->page_size == 16 ? 16u : 32u};
+  const cuuint32_t es[2] = {1, 1};
+  return enc(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+             const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             cols * elem == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kPgMinTiles = 4;  // shortest run of a team, in tiles of 32 keys
+
+struct PagedPlan {
+  int rows, R, teams;  // query rows per KV head, warps per team, teams of a full grid
+  size_t part_o, part_ml, cut, total;
+};
+
+ra_status check_queries(int B, int Tq, int Hq, int Hkv, int D) {
+  if (B < 1 || Tq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return RA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return RA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(Hq / Hkv) * Tq > kDecMaxRows) return RA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * Tq * Hq > 0x7fffffffLL) return RA_ERR_UNSUPPORTED;
+  return RA_OK;
+}
+
+PagedPlan paged_plan(int B, int Tq, int Hq, int Hkv, int D) {
+  PagedPlan p;
+  p.rows = (Hq / Hkv) * Tq;
+  p.R = p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
+  p.teams = sm_count() * (kPgWarps / p.R);
+  p.part_o = 0;
+  p.part_ml = align256(static_cast<size_t>(p.teams) * 2 * p.rows * D * 4);
+  p.cut = align256(p.part_ml + static_cast<size_t>(p.teams) * 2 * p.rows * 8);
+  p.total = align256(p.cut + static_cast<size_t>(B) * Hkv * 8);
+  return p;
+}
+
+template <int D, int WPR>
+ra_status launch_paged_combine(const PagedArgs& a, int teams, cudaStream_t st) {
+  const long long rows = static_cast<long long>(a.bt.B) * a.bt.Hkv * a.rows;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 8 / WPR - 1) / (8 / WPR)), 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, WPR>, a, teams));
+}
+
+template <int D, int ET>
+ra_status launch_paged_t(PagedArgs a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
+  using SL = PgSmem<D, ET>;
+  static int attr_set[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !attr_set[dev]) {
+    if (cudaFuncSetAttribute(paged_partial_kernel<D, ET>, cudaFuncAttributeMaxDynamicSharedMemorySize, SL::kBytes) !=
+        cudaSuccess)
+      return RA_ERR_CUDA;
+    if (dev < 64) attr_set[dev] = 1;
+  }
+  a.slots = a.R * kPgRing / SL::kItem;
+  if (a.slots > kPgSlots * a.R) a.slots = kPgSlots * a.R;
+  // the longest line that the table (or the selection) allows
+  const long long pages = a.selected && a.n_sel < a.bt.max_pages ? a.n_sel : a.bt.max_pages;
+  const long long tiles = ((pages << a.bt.page_shift) + kPgKeys - 1) / kPgKeys;
+  const long long line = tiles * a.bt.B * a.bt.Hkv;
+  const long long runs = (line + a.min_tiles - 1) / a.min_tiles;
+  const int grid = static_cast<int>(runs < sm_count() ? runs : sm_count());
+  paged_partial_kernel<D, ET><<<grid, kPgThreads, SL::kBytes, st>>>(mk, mv, a);
+  const ra_status s = cuda_status(cudaGetLastError());
+  if (s != RA_OK) return s;
+  // a row's parts: 8 warps where rows are few, one where they alone fill the GPU
+  const long long rows = static_cast<long long>(a.bt.B) * a.bt.Hkv * a.rows;
+  const int teams = grid * (kPgWarps / a.R);
+  return rows <= 2048 ? launch_paged_combine<D, 8>(a, teams, st) : launch_paged_combine<D, 1>(a, teams, st);
+}
+
+template <int D>
+ra_status launch_paged_d(const PagedArgs& a, int et, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
+  if (et == kCacheBf16) return launch_paged_t<D, kCacheBf16>(a, mk, mv, st);
+  if (et == kCacheI8) return launch_paged_t<D, kCacheI8>(a, mk, mv, st);
+  return launch_paged_t<D, kCacheE4M3>(a, mk, mv, st);
 }
 
 }  // namespace
@@ -133,6 +231,54 @@ ra_status ra_cache_read(const ra_paged_cache* cache, int first, int T, void* k, 
   if (out_dtype == RA_BF16)
     return cache->D == 128 ? launch_read_t<128, __nv_bfloat16>(a, et, g, st) : launch_read_t<64, __nv_bfloat16>(a, et, g, st);
   return cache->D == 128 ? launch_read_t<128, float>(a, et, g, st) : launch_read_t<64, float>(a, et, g, st);
+}
+
+size_t ra_paged_decode_workspace(int B, int Tq, int Hq, int Hkv, int D) {
+  if (check_queries(B, Tq, Hq, Hkv, D) != RA_OK) return static_cast<size_t>(-1);
+  return paged_plan(B, Tq, Hq, Hkv, D).total;
+}
+
+ra_status ra_paged_decode_attention(const void* q, ra_dtype in_dtype, const ra_paged_cache* cache, int Tq, int Hq,
+                                    int causal, const int32_t* selected, int n_sel, void* out, ra_dtype out_dtype,
+                                    float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  ra_status s = check_cache(cache);
+  if (s != RA_OK) return s;
+  s = check_queries(cache->B, Tq, Hq, cache->Hkv, cache->D);
+  if (s != RA_OK) return s;
+  if (in_dtype != RA_BF16) return in_dtype == RA_F32 ? RA_ERR_UNSUPPORTED : RA_ERR_INVALID_ARG;
+  if (out_dtype != RA_F32 && out_dtype != RA_BF16) return RA_ERR_INVALID_ARG;
+  if (!q || !out || !lse || !aligned16(q) || !aligned16(out) || !aligned4(lse)) return RA_ERR_INVALID_ARG;
+  if (selected ? n_sel < 1 || !aligned4(selected) : n_sel != 0) return RA_ERR_INVALID_ARG;
+  const PagedPlan p = paged_plan(cache->B, Tq, Hq, cache->Hkv, cache->D);
+  if (!workspace || workspace_bytes < p.total) return RA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255) return RA_ERR_INVALID_ARG;
+  CUtensorMap mk, mv;
+  if (!make_page_map(&mk, cache->k_pages, cache) || !make_page_map(&mv, cache->v_pages, cache)) return RA_ERR_CUDA;
+  PagedArgs a;
+  memset(&a, 0, sizeof(a));
+  a.bt = batch_of(cache, Tq);
+  a.Hq = Hq;
+  a.groups = Hq / cache->Hkv;
+  a.rows = p.rows;
+  a.causal = causal != 0;
+  a.R = p.R;
+  a.min_tiles = kPgMinTiles;
+  a.n_sel = n_sel;
+  a.selected = selected;
+  a.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(cache->D)));
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k_scales = cache->k_scales;
+  a.v_scales = cache->v_scales;
+  char* ws = static_cast<char*>(workspace);
+  a.part_o = reinterpret_cast<float*>(ws + p.part_o);
+  a.part_ml = reinterpret_cast<float2*>(ws + p.part_ml);
+  a.cut = reinterpret_cast<int2*>(ws + p.cut);
+  a.out = out;
+  a.out_bf16 = out_dtype == RA_BF16;
+  a.lse = lse;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int et = cache_code(cache->dtype);
+  return cache->D == 128 ? launch_paged_d<128>(a, et, mk, mv, st) : launch_paged_d<64>(a, et, mk, mv, st);
 }
 
 }  // extern "C"

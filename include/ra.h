@@ -323,7 +323,7 @@ int ra_decode_splits(int B, int Tq, int Skv, int Hq, int Hkv, int D, int n_split
  *  page_table  device int32 [B, max_pages]: page of tokens [i page_size,
  *             (i + 1) page_size) of a sequence.  Entries behind a sequence's
  *             last token are not read.
- *  B, max_pages  sequences; table entries of each (max_pages * page_size < 2^31).
+ *  B, max_pages  sequences; table entries of each (max_pages * page_size <= 2^31 - 256).
  *  seq_lens   device int32 [B]: tokens of each sequence in the cache, the new
  *             ones of this step included; 0 for an empty slot.
  *  new_lens   device int32 [B], 0 <= new_lens[b] <= min(T, seq_lens[b]): how
@@ -381,6 +381,42 @@ ra_status ra_cache_append(const ra_paged_cache* cache, const void* k, const void
  */
 ra_status ra_cache_read(const ra_paged_cache* cache, int first, int T, void* k, void* v, ra_dtype out_dtype,
                         void* stream);
+
+/*
+ * ra_paged_decode_attention - attention of the new tokens' queries over a paged
+ * cache, all of it or the selected pages of each KV head.
+ * [TR] "Reading between the lines": the decode phase as KV-cache chunking, the
+ * chunks' partial results joined by their log-sum-exp.
+ *  q          device, bf16, [B, Tq, Hq, D]; in_dtype must be RA_BF16.  Row
+ *             i < new_lens[b] is the token at position p = seq_lens[b] -
+ *             new_lens[b] + i (its key and value already appended).
+ *  cache      as above; key_bounds is not used.
+ *  Hq         Hq % Hkv == 0; query head h reads KV head h / (Hq / Hkv);
+ *             (Hq / Hkv) * Tq <= 64 (else RA_ERR_UNSUPPORTED).
+ *  causal     nonzero: row i sees keys j <= p; else keys j < seq_lens[b].
+ *  selected   device int32 [B, Hkv, n_sel], or NULL (n_sel = 0) for the whole
+ *             cache: table indices of the pages that each KV head sees, strictly
+ *             ascending, -1 for no page.  Of each list the first min(n_sel,
+ *             ceil(seq_lens[b] / page_size)) entries are read; one that is out of
+ *             range or does not ascend is recorded as RA_ERR_DEVICE_BOUNDS and
+ *             counts as -1.
+ *  out, lse   device, out_dtype (RA_F32 or RA_BF16, nearest even) [B, Tq, Hq, D]
+ *             and fp32 [B, Tq, Hq], every row written.  A row that is not
+ *             real or sees no key gets out = 0, lse = -inf.  What masked places
+ *             hold (NaN, infinities, memory never written) has no effect.
+ *  workspace  device scratch of ra_paged_decode_workspace() bytes, 256-byte
+ *             aligned; its contents need no preparation.  Calls that may run at
+ *             the same time need one each.
+ * No atomics: the result does not depend on scheduling.  The call reads the
+ * lengths on the device; captured in a graph, it replays with those then in place.
+ */
+ra_status ra_paged_decode_attention(const void* q, ra_dtype in_dtype, const ra_paged_cache* cache, int Tq, int Hq,
+                                    int causal, const int32_t* selected, int n_sel, void* out, ra_dtype out_dtype,
+                                    float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of ra_paged_decode_attention, for any lengths ((size_t)-1
+ * when the arguments are invalid). */
+size_t ra_paged_decode_workspace(int B, int Tq, int Hq, int Hkv, int D);
 
 /*
  * ra_ring_attention_backward - gradients of ra_ring_attention.

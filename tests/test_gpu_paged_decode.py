@@ -1,0 +1,330 @@
+"""ra_paged_decode_attention against the fp64 oracle.
+
+Tolerances, from the arithmetic (per case, on the case's own values):
+  scores   fp32 sums of D exact products of bf16 values, scaled: an error of at
+           most dx = (D + 4) 2^-24 max_j s sum_d |q_d k_jd|;
+  weights  2^dx ... and two bf16 terms (2^-17) for a bf16 output, three for fp32
+           (2^-24), the exponential itself 2^-21;
+  sums     n terms in fp32: n 2^-24;
+so |out - exact| <= 2 (dx + w + 2^-21 + n 2^-24) max|v| + half a step of the
+output type of |out|, and |lse - exact| <= dx + 2^-21 + n 2^-24 + 2^-23 |lse|."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as P
+
+pytestmark = pytest.mark.gpu
+
+TORCH = {"bf16": torch.bfloat16, "int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+
+
+def f64(t):
+    return t.detach().cpu().to(torch.float64).numpy()
+
+
+class Case:
+    """A filled cache: the valid rows hold drawn tokens, every other row of the
+    pages NaN (bf16) or random codes with NaN scales."""
+
+    def __init__(self, dtype, B, Tq, Hq, Hkv, D, ps, seq, new=None, seed=0, extra=2):
+        gen = torch.Generator().manual_seed(seed)
+        self.seq, self.ps, self.dtype = seq, ps, dtype
+        self.new = new if new is not None else [min(Tq, n) for n in seq]
+        need = [-(-n // ps) for n in seq]
+        n_pages = sum(need) + extra
+        order = torch.randperm(n_pages, generator=gen).to(torch.int32)
+        self.table = torch.full((B, max(max(need), 1)), -1, dtype=torch.int32)
+        at = 0
+        for b, c in enumerate(need):
+            self.table[b, :c] = order[at:at + c]
+            at += c
+        self.ref = P.Cache(n_pages, Hkv, ps, D, dtype)
+        T = max(max(seq), 1)
+        gain = torch.exp(0.5 * torch.randn(D, generator=gen))
+        k = (torch.randn((B, T, Hkv, D), generator=gen) * gain).to(torch.bfloat16)
+        v = torch.randn((B, T, Hkv, D), generator=gen).to(torch.bfloat16)
+        P.append(self.ref, f64(k), f64(v), self.table.tolist(), seq, seq)
+        self.q = (1.5 * torch.randn((B, Tq, Hq, D), generator=gen)).to(torch.bfloat16)
+        live = np.zeros((n_pages, ps), bool)
+        for b, n in enumerate(seq):
+            for p in range(n):
+                live[int(self.table[b, p // ps]), p % ps] = True
+        dead = torch.tensor(~live)[:, None, :].expand(n_pages, Hkv, ps)
+        self.pages, self.scales = {}, {"k": None, "v": None}
+        for w in "kv":
+            if dtype == "bf16":
+                x = torch.tensor(self.ref.value[w]).to(torch.bfloat16)
+                x[dead] = float("nan")
+                self.pages[w] = x.cuda()
+            else:
+                c = torch.tensor(self.ref.code[w])
+                c[dead] = 0x7e
+                s = torch.tensor(self.ref.scale[w]).float()
+                s[dead] = float("nan")
+                self.pages[w] = c.view(TORCH[dtype]).cuda()
+                self.scales[w] = s.cuda()
+        self.args = (self.q.cuda(), self.pages["k"], self.pages["v"], self.table.cuda(),
+                     torch.tensor(seq, dtype=torch.int32).cuda())
+        self.kw = dict(new_lens=None if new is None else torch.tensor(new, dtype=torch.int32).cuda(),
+                       k_scales=self.scales["k"], v_scales=self.scales["v"])
+
+    def expect(self, causal, selected=None):
+        sel = None if selected is None else selected.cpu().tolist()
+        return P.decode(f64(self.q), self.ref, self.table.tolist(), self.seq, self.new, causal, sel)
+
+    def check(self, got, causal, selected=None, what=""):
+        out, lse = got
+        ro, rl = self.expect(causal, selected)
+        D = self.q.shape[-1]
+        q, k, v = np.abs(f64(self.q)), np.abs(self.ref.value["k"]), np.abs(self.ref.value["v"])
+        dx = (D + 4) * 2.0 ** -24 * (q.reshape(-1, D).max(0) * k.reshape(-1, D).max(0)).sum() / math.sqrt(D)
+        n = max(self.seq + [1]) * 2.0 ** -24
+        w = 2.0 ** -17 if out.dtype == torch.bfloat16 else 2.0 ** -24
+        half = torch.finfo(out.dtype).eps / 2
+        tol = 2 * (dx + w + 2.0 ** -21 + n) * v.max() + half * np.abs(ro) * 1.01
+        go, gl = f64(out), f64(lse)
+        assert np.array_equal(np.isneginf(gl), np.isneginf(rl)), what
+        assert np.isfinite(go).all(), what
+        assert (np.abs(go - ro) <= tol).all(), f"{what}: out off by {np.max(np.abs(go - ro) / tol):.3g} tolerances"
+        fin = np.isfinite(rl)
+        off = np.abs(gl[fin] - rl[fin]) - (dx + 2.0 ** -21 + n + 2.0 ** -23 * np.abs(rl[fin]))
+        assert (off <= 0).all(), f"{what}: lse off by {off.max():.3g} more than it may"
+        assert (go[np.isneginf(rl)] == 0).all(), what
+
+
+SHAPES = [
+    # B, Tq, Hq, Hkv, D, ps, seq, new
+    (1, 1, 1, 1, 64, 16, [1], None),
+    (1, 1, 8, 2, 128, 16, [1000], None),
+    (2, 1, 4, 4, 128, 32, [31, 33], None),
+    (4, 1, 8, 1, 64, 64, [64, 0, 65, 200], None),
+    (3, 4, 8, 2, 128, 16, [100, 3, 47], None),                 # fewer tokens than query rows
+    (3, 4, 8, 2, 64, 128, [300, 128, 129], [2, 4, 1]),         # a padded batch
+    (2, 5, 12, 3, 128, 32, [77, 160], [5, 0]),                 # 20 rows: two warps to a team; an idle sequence
+    (1, 7, 14, 2, 64, 16, [333], None),                        # 49 rows: four warps
+    (2, 1, 64, 1, 128, 64, [1500, 17], None),                  # 64 rows
+    (2, 2, 32, 1, 128, 16, [700, 699], None),
+    (5, 1, 7, 7, 128, 128, [1, 127, 128, 129, 640], None),
+    (20, 1, 4, 2, 128, 16, [0, 0, 5, 900] + [33] * 15 + [0], None),
+    (70, 2, 4, 4, 64, 32, [0] * 40 + [9, 2000] + [40] * 27 + [1], None),   # empty runs longer than a warp
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "int8", "e4m3"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "-".join(str(x) for x in s[:6]))
+@pytest.mark.parametrize("causal", [True, False])
+def test_paged_decode(cuda_lib, dtype, shape, causal):
+    ra = cuda_lib
+    c = Case(dtype, *shape, seed=shape[0] + 7 * shape[1])
+    for odt in (torch.bfloat16, torch.float32):
+        got = ra.ra_paged_decode_attention(*c.args, causal=causal, out_dtype=odt, **c.kw)
+        c.check(got, causal, what=str(odt))
+        again = ra.ra_paged_decode_attention(*c.args, causal=causal, out_dtype=odt, **c.kw)
+        assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "int8", "e4m3"])
+@pytest.mark.parametrize("D,ps,Hkv,G", [(128, 16, 2, 4), (64, 128, 1, 1), (128, 64, 3, 7)])
+def test_many_cut_pairs(cuda_lib, dtype, D, ps, Hkv, G):
+    """Long beside short: pairs cut over many teams, several pairs in one team's run."""
+    ra = cuda_lib
+    c = Case(dtype, 6, 1, Hkv * G, Hkv, D, ps, [9001, 40, 1, 0, 3333, 700], seed=4)
+    got = ra.ra_paged_decode_attention(*c.args, out_dtype=torch.bfloat16, **c.kw)
+    c.check(got, True)
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "int8", "e4m3"])
+@pytest.mark.parametrize("ps", [16, 32, 64, 128])
+def test_selected_pages(cuda_lib, dtype, ps):
+    ra = cuda_lib
+    Hkv, n_sel = 2, 5
+    c = Case(dtype, 4, 2, 8, Hkv, 128, ps, [ps * 20 + 3, ps * 3, 1, 0], seed=ps)
+    gen = torch.Generator().manual_seed(ps)
+    sel = torch.full((4, Hkv, n_sel), -1, dtype=torch.int32)
+    for b, n in enumerate(c.seq):
+        pages = -(-n // ps)
+        for h in range(Hkv):
+            m = min(n_sel, pages) - (1 if h and pages > 1 else 0)
+            sel[b, h, :m] = torch.randperm(pages, generator=gen)[:m].sort().values.int()
+    sel[0, 1] = torch.tensor([-1, 0, -1, 7, 20], dtype=torch.int32)  # no page, in the middle of a list
+    for causal in (True, False):
+        for odt in (torch.bfloat16, torch.float32):
+            got = ra.ra_paged_decode_attention(*c.args, causal=causal, selected=sel.cuda(), out_dtype=odt, **c.kw)
+            c.check(got, causal, sel)
+    assert ra.ra_get_device_status() == ra.RA_OK
+    none = torch.full_like(sel, -1).cuda()  # lists without a page: no row sees a key
+    out, lse = ra.ra_paged_decode_attention(*c.args, selected=none, **c.kw)
+    assert not out.any() and torch.isneginf(lse).all()
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
+def test_selected_lists_that_break_the_rule_are_recorded(cuda_lib):
+    """An index out of range, the same one twice, a descending list: recorded, counted as no page."""
+    ra = cuda_lib
+    c = Case("bf16", 1, 1, 4, 1, 64, 16, [100], seed=2)
+    for bad, same_as in (([0, 0, 3], [0, -1, 3]), ([5, 2, 6], [5, -1, 6]), ([1, 7, -1], [1, -1, -1]), ([-7, 2, 3], [-1, 2, 3])):
+        sel = torch.tensor([[bad]], dtype=torch.int32)
+        got = ra.ra_paged_decode_attention(*c.args, selected=sel.cuda(), **c.kw)
+        assert ra.ra_get_device_status() == ra.RA_ERR_DEVICE_BOUNDS
+        c.check(got, True, torch.tensor([[same_as]]))
+
+
+def test_bad_table_and_lengths_are_recorded(cuda_lib):
+    ra = cuda_lib
+    c = Case("int8", 3, 2, 4, 2, 128, 16, [40, 70, 33], seed=3)
+    good = ra.ra_paged_decode_attention(*c.args, **c.kw)
+    assert ra.ra_get_device_status() == ra.RA_OK
+    q, kp, vp, table, seq = c.args
+    for value in (-1, kp.shape[0], 1 << 30):
+        t = table.clone()
+        t[1, 2] = value
+        out, lse = ra.ra_paged_decode_attention(q, kp, vp, t, seq, **c.kw)
+        assert ra.ra_get_device_status() == ra.RA_ERR_DEVICE_BOUNDS
+        for b in (0, 2):  # the other sequences are as they were
+            assert torch.equal(out[b], good[0][b]) and torch.equal(lse[b], good[1][b])
+    for n in (-5, 10 ** 6):
+        s = seq.clone()
+        s[1] = n
+        ra.ra_paged_decode_attention(q, kp, vp, table, s, **c.kw)
+        assert ra.ra_get_device_status() == ra.RA_ERR_DEVICE_BOUNDS
+
+
+def test_infinities_and_nan_of_tokens_behind_a_row(cuda_lib):
+    """Causal rows of one call: a token's NaN key or infinite value reaches its own
+    and later rows only."""
+    ra = cuda_lib
+    c = Case("bf16", 1, 4, 4, 2, 64, 16, [50], seed=6)
+    where = int(c.table[0, 3]), 49 % 16  # the last token
+    c.pages["v"][where[0], :, where[1]] = float("inf")
+    c.pages["k"][where[0], 0, where[1]] = float("nan")
+    out, lse = ra.ra_paged_decode_attention(*c.args, out_dtype=torch.float32, **c.kw)
+    ro, rl = c.expect(True)
+    assert np.allclose(f64(out)[:, :3], ro[:, :3], atol=1e-4) and np.allclose(f64(lse)[:, :3], rl[:, :3], atol=1e-4)
+    assert torch.isnan(out[0, 3, :2]).all()                      # KV head 0: the key is NaN
+    assert torch.isinf(out[0, 3, 2:]).all()                      # KV head 1: the value is infinite
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
+def test_a_nan_scale_is_a_nan_row(cuda_lib):
+    ra = cuda_lib
+    c = Case("int8", 1, 2, 2, 1, 128, 32, [90], seed=6)
+    page = int(c.table[0, 2])
+    c.scales["v"][page, 0, 89 % 32] = float("nan")  # the last token's value
+    out, _ = ra.ra_paged_decode_attention(*c.args, out_dtype=torch.float32, **c.kw)
+    assert torch.isfinite(out[0, 0]).all() and torch.isnan(out[0, 1]).all()
+
+
+def test_scores_of_every_size(cuda_lib):
+    """Scores in the thousands, both signs: the running maximum carries them."""
+    ra = cuda_lib
+    for sign in (1.0, -1.0):
+        c = Case("bf16", 1, 1, 4, 2, 128, 16, [400], seed=9)
+        c.q = (c.q.float() * 60 * sign).to(torch.bfloat16)
+        c.args = (c.q.cuda(),) + c.args[1:]
+        c.check(ra.ra_paged_decode_attention(*c.args, out_dtype=torch.float32, **c.kw), True)
+
+
+def test_offsets_past_32_bits(cuda_lib):
+    """Pages whose byte and element offsets pass 2^32 and 2^31."""
+    ra = cuda_lib
+    D, Hkv, ps = 128, 2, 64
+    for dtype, n_pages in (("bf16", 140000), ("int8", 140000)):  # 17.9M rows: 2.3G elements
+        c = Case(dtype, 2, 1, 4, Hkv, D, ps, [200, 65], seed=1)
+        small = c.pages["k"].shape[0]
+        off = n_pages - small
+        big, scales = {}, {"k": None, "v": None}
+        for w in "kv":
+            big[w] = torch.empty((n_pages, Hkv, ps, D), dtype=c.pages[w].dtype, device="cuda")
+            big[w][off:] = c.pages[w]
+            if dtype != "bf16":
+                scales[w] = torch.empty((n_pages, Hkv, ps), device="cuda")
+                scales[w][off:] = c.scales[w]
+        table = torch.where(c.table >= 0, c.table + off, -1).int().cuda()
+        lens = c.args[4]
+        got = ra.ra_paged_decode_attention(c.args[0], big["k"], big["v"], table, lens, k_scales=scales["k"],
+                                           v_scales=scales["v"], out_dtype=torch.bfloat16)
+        c.check(got, True)
+        gk, gv = ra.ra_cache_read(big["k"], big["v"], table, lens, 200, k_scales=scales["k"], v_scales=scales["v"],
+                                  out_dtype=torch.float32)
+        rk, rv = ra.ra_cache_read(c.pages["k"], c.pages["v"], c.table.cuda(), lens, 200, k_scales=c.scales["k"],
+                                  v_scales=c.scales["v"], out_dtype=torch.float32)
+        assert torch.equal(gk, rk) and torch.equal(gv, rv)
+        new = torch.ones((2, 1, Hkv, D), dtype=torch.bfloat16, device="cuda")
+        ra.ra_cache_append(new, new, big["k"], big["v"], table, lens, k_scales=scales["k"], v_scales=scales["v"])
+        gk, _ = ra.ra_cache_read(big["k"], big["v"], table, lens, 200, k_scales=scales["k"], v_scales=scales["v"],
+                                 out_dtype=torch.float32)
+        assert torch.equal(gk[0, :199], rk[0, :199]) and torch.allclose(gk[0, 199], torch.ones(()).cuda())
+        assert torch.allclose(gk[1, 64], torch.ones(()).cuda())
+        assert ra.ra_get_device_status() == ra.RA_OK
+        del big, scales, gk, gv, rk, rv
+        torch.cuda.empty_cache()
+
+
+def test_graph_stream_and_workspace(cuda_lib):
+    """Two captured calls that share a workspace, replayed in turn with other
+    lengths; a call on another stream; a workspace full of NaN."""
+    ra = cuda_lib
+    a = Case("bf16", 3, 1, 8, 2, 128, 16, [600, 100, 900], seed=1)
+    b = Case("e4m3", 2, 3, 8, 1, 64, 32, [300, 1000], seed=2)
+    need = max(ra.ra_paged_decode_workspace(3, 1, 8, 2, 128), ra.ra_paged_decode_workspace(2, 3, 8, 1, 64))
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    got, graphs = [], []
+    for c in (a, b):
+        ra.ra_paged_decode_attention(*c.args, workspace=ws, **c.kw)
+    torch.cuda.synchronize()
+    for c in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(ra.ra_paged_decode_attention(*c.args, workspace=ws, out_dtype=torch.bfloat16, **c.kw))
+        graphs.append(g)
+    for lens in ([600, 100, 900], [1, 0, 512], [599, 64, 33]):
+        a.seq, a.new = lens, [min(1, n) for n in lens]
+        a.args[4].copy_(torch.tensor(lens, dtype=torch.int32))
+        ws.fill_(255)
+        for g in graphs:
+            g.replay()
+        a.check(got[0], True)
+        b.check(got[1], True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    res = ra.ra_paged_decode_attention(*b.args, stream=side, out_dtype=torch.bfloat16, **b.kw)
+    side.synchronize()
+    b.check(res, True)
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
+def test_a_serving_run(cuda_lib):
+    """Prompt, appended in chunks; then decoded token by token: the paged calls
+    against the dense decode over the same (bf16) cache, and ra_ring_attention over
+    the prefix read back."""
+    ra = cuda_lib
+    gen = torch.Generator().manual_seed(12)
+    B, Hq, Hkv, D, ps, S, steps = 2, 8, 2, 128, 16, 96, 5
+    k, v = (torch.randn((B, S + steps, Hkv, D), generator=gen).to(torch.bfloat16).cuda() for _ in "kv")
+    q = torch.randn((B, S + steps, Hq, D), generator=gen).to(torch.bfloat16).cuda()
+    n_pages = 2 * (-(-(S + steps) // ps))
+    table = torch.randperm(n_pages, generator=gen).to(torch.int32).view(B, -1).contiguous().cuda()
+    kp = torch.full((n_pages, Hkv, ps, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    vp = kp.clone()
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    for s0, s1 in ((0, 41), (41, 43), (43, S)):
+        lens.fill_(s1)
+        ra.ra_cache_append(k[:, s0:s1].contiguous(), v[:, s0:s1].contiguous(), kp, vp, table, lens)
+    rk, rv = ra.ra_cache_read(kp, vp, table, lens, S)
+    assert torch.equal(rk, k[:, :S]) and torch.equal(rv, v[:, :S])
+    full, _ = ra.ra_ring_attention(q[:, :S].contiguous(), rk, rv, 4, True)
+    last, _ = ra.ra_paged_decode_attention(q[:, S - 1:S].contiguous(), kp, vp, table, lens)
+    assert torch.allclose(full[:, S - 1:], last, atol=2e-2)
+    for t in range(S, S + steps):
+        lens.fill_(t + 1)
+        one = slice(t, t + 1)
+        ra.ra_cache_append(k[:, one].contiguous(), v[:, one].contiguous(), kp, vp, table, lens)
+        got = ra.ra_paged_decode_attention(q[:, one].contiguous(), kp, vp, table, lens)
+        want = ra.ra_decode_attention(q[:, one].contiguous(), k[:, :t + 1].contiguous(), v[:, :t + 1].contiguous())
+        assert torch.allclose(got[0], want[0], atol=2e-2) and torch.allclose(got[1], want[1], atol=1e-4)
+    assert ra.ra_get_device_status() == ra.RA_OK

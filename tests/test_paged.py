@@ -88,6 +88,42 @@ def test_binding_refuses_tensors_on_the_host(ra):
         ra.ra_cache_read(k, k, table, lens, 4)
 
 
+def decode(ra, c, q=FAKE, in_dtype=1, Tq=1, Hq=8, causal=1, selected=None, n_sel=0, out=FAKE, out_dtype=1, lse=FAKE,
+           ws=FAKE, ws_bytes=1 << 40):
+    return ra._lib.ra_paged_decode_attention(q, in_dtype, ctypes.byref(c), Tq, Hq, causal, selected, n_sel, out,
+                                             out_dtype, lse, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,status", BAD_CACHE)
+def test_paged_decode_refuses_a_bad_cache(ra, kw, status):
+    assert decode(ra, cache(ra, **kw)) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), 1), (dict(q=FAKE + 8), 1), (dict(out=None), 1), (dict(out=FAKE + 4), 1), (dict(lse=None), 1),
+    (dict(lse=FAKE + 2), 1), (dict(in_dtype=0), 2), (dict(in_dtype=2), 1), (dict(out_dtype=2), 1), (dict(Tq=0), 1),
+    (dict(Hq=7), 1), (dict(Hq=0), 1),
+    (dict(Hq=66, Tq=2), 2),                                       # 33 heads x 2 tokens > 64 rows per KV head
+    (dict(Hq=2, Tq=65), 2),
+    (dict(Hq=2, Tq=1 << 30), 2),
+    (dict(selected=FAKE, n_sel=0), 1), (dict(selected=FAKE, n_sel=-1), 1), (dict(selected=FAKE + 2, n_sel=4), 1),
+    (dict(n_sel=4), 1),                                           # a count without a list
+    (dict(ws=None), 3), (dict(ws_bytes=64), 3), (dict(ws=FAKE + 64), 1)])
+def test_paged_decode_refuses(ra, kw, status):
+    assert decode(ra, cache(ra), **kw) == status
+
+
+def test_paged_decode_workspace(ra):
+    # teams of a full grid: 8 warps an SM, 1, 2 or 4 to a team; two cut pairs each
+    for Tq, Hq, Hkv, per in ((1, 8, 2, 8), (4, 32, 8, 8), (5, 4, 1, 4), (1, 64, 1, 2)):
+        rows = Hq // Hkv * Tq
+        n = ra.ra_paged_decode_workspace(3, Tq, Hq, Hkv, 128)
+        assert n >= 148 * per * 2 * rows * (128 + 2) * 4 + 3 * Hkv * 8
+    for bad in ((0, 1, 8, 2, 128), (1, 1, 8, 3, 128), (1, 1, 8, 2, 96), (1, 65, 8, 8, 128)):
+        with pytest.raises(ra.RAError):
+            ra.ra_paged_decode_workspace(*bad)
+
+
 # ------------------------------------------------------------- oracle pins
 
 def test_e4m3_grid_is_the_types():
