@@ -52,7 +52,7 @@ EXPORTED = ["ra_block_attn", "ra_block_attn_merge", "ra_merge_partial", "ra_merg
             "ra_decode_attention", "ra_decode_workspace", "ra_decode_splits", "ra_ring_attention_backward",
             "ra_ring_attention_backward_workspace", "ra_debug_build", "ra_get_bounds_record",
             "ra_set_cta_timeline", "ra_cache_append", "ra_cache_read",
-            "ra_paged_decode_attention", "ra_paged_decode_workspace"]
+            "ra_paged_decode_attention", "ra_paged_decode_workspace", "ra_page_select", "ra_page_select_workspace"]
 
 RA_TIMELINE_ATTN_FWD, RA_TIMELINE_BWD_DKV, RA_TIMELINE_BWD_DQ = 0, 1, 2
 TIMELINE_KERNELS = {"attn_fwd": RA_TIMELINE_ATTN_FWD, "bwd_dkv": RA_TIMELINE_BWD_DKV, "bwd_dq": RA_TIMELINE_BWD_DQ}
@@ -127,6 +127,10 @@ _lib.ra_paged_decode_attention.argtypes = [_vp, _i, ctypes.POINTER(ra_paged_cach
 _lib.ra_paged_decode_attention.restype = _i
 _lib.ra_paged_decode_workspace.argtypes = [_i, _i, _i, _i, _i]
 _lib.ra_paged_decode_workspace.restype = _sz
+_lib.ra_page_select.argtypes = [_vp, _i, ctypes.POINTER(ra_paged_cache), _i, _i, _i, _vp, _vp, _sz, _vp]
+_lib.ra_page_select.restype = _i
+_lib.ra_page_select_workspace.argtypes = [_i, _i, _i]
+_lib.ra_page_select_workspace.restype = _sz
 
 
 class RAError(RuntimeError):
@@ -560,3 +564,40 @@ def ra_paged_decode_attention(q, k_pages, v_pages, page_table, seq_lens, new_len
              _expect(out, "out", odt, shape, dev), _dtype_code(odt), _expect(lse, "lse", torch.float32, shape[:3], dev),
              _ptr(workspace), workspace.numel() * workspace.element_size())
     return out, lse
+
+
+def ra_page_select_workspace(B, Hkv, max_pages) -> int:
+    n = _lib.ra_page_select_workspace(B, Hkv, max_pages)
+    if n == ctypes.c_size_t(-1).value:
+        raise RAError(RA_ERR_INVALID_ARG, "ra_page_select_workspace")
+    return n
+
+
+def ra_page_select(q, key_bounds, page_table, seq_lens, n_sel: int, page_size: int, new_lens=None, selected=None,
+                   workspace=None, stream=None):
+    """The n_sel best pages of each sequence and KV head for the new tokens'
+    queries q [B, Tq, Hq, D] (bf16) by the bound that key_bounds
+    [n_pages, Hkv, 2, D] puts on a page's scores: int32 [B, Hkv, n_sel],
+    ascending, -1 behind.  The new tokens' own pages are always among them."""
+    dev = key_bounds.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be contiguous CUDA tensors")
+    if q.dim() != 4 or key_bounds.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("q must be [B, Tq, Hq, D], key_bounds [n_pages, Hkv, 2, D], page_table [B, max_pages]")
+    n_pages, Hkv, _, D = key_bounds.shape
+    B, max_pages = page_table.shape
+    _, Tq, Hq, _ = q.shape
+    i32 = torch.int32
+    c = ra_paged_cache(None, None, None, None,
+                       _expect(key_bounds, "key_bounds", torch.bfloat16, (n_pages, Hkv, 2, D), dev), RA_BF16, n_pages,
+                       page_size, Hkv, D, _expect(page_table, "page_table", i32, page_table.shape, dev), B, max_pages,
+                       _expect(seq_lens, "seq_lens", i32, (B,), dev), _expect(new_lens, "new_lens", i32, (B,), dev))
+    if selected is None:
+        selected = torch.empty((B, Hkv, max(n_sel, 0)), dtype=i32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(ra_page_select_workspace(B, Hkv, max_pages), dtype=torch.uint8, device=dev)
+    _call_on(dev, stream, _lib.ra_page_select, "ra_page_select", _expect(q, "q", q.dtype, (B, Tq, Hq, D), dev),
+             _dtype_code(q.dtype), ctypes.byref(c), Tq, Hq, n_sel,
+             _expect(selected, "selected", i32, (B, Hkv, n_sel), dev), _ptr(workspace),
+             workspace.numel() * workspace.element_size())
+    return selected

@@ -2,6 +2,7 @@
 // argument validation and launches.  Included by api.cu, whose helpers it uses.
 #pragma once
 
+#include "page_select.cuh"
 #include "paged.cuh"
 #include "paged_decode.cuh"
 
@@ -169,6 +170,30 @@ ra_status launch_paged_d(const PagedArgs& a, int et, const CUtensorMap& mk, cons
   return launch_paged_t<D, kCacheE4M3>(a, mk, mv, st);
 }
 
+// Most pages that T consecutive tokens touch.
+int page_span(int T, int page_size) {
+  return static_cast<int>((static_cast<long long>(T) + page_size - 2) / page_size) + 1;
+}
+
+template <int D>
+ra_status launch_select_d(const SelectArgs& a, cudaStream_t st) {
+  const unsigned blocks = static_cast<unsigned>((a.bt.max_pages + kScoreThreads - 1) / kScoreThreads);
+  page_score_kernel<D><<<dim3(blocks, a.bt.Hkv, a.bt.B), kScoreThreads, 0, st>>>(a);
+  const ra_status s = cuda_status(cudaGetLastError());
+  if (s != RA_OK) return s;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(static_cast<unsigned>(a.bt.B) * a.bt.Hkv, 1, 1);
+  cfg.blockDim = dim3(kSelThreads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, page_select_kernel, a));
+}
+
 }  // namespace
 
 extern "C" {
@@ -190,7 +215,7 @@ ra_status ra_cache_append(const ra_paged_cache* cache, const void* k, const void
   a.v_scales = cache->v_scales;
   a.bounds = static_cast<__nv_bfloat16*>(cache->key_bounds);
   const int ps = cache->page_size;
-  a.span = static_cast<int>((static_cast<long long>(T) - 1 + ps - 1) / ps) + 1;
+  a.span = page_span(T, ps);
   a.wpu = 1;  // about 16 rows for each warp of a unit
   while (a.wpu * 16 < ps && a.wpu * 16 < T) a.wpu *= 2;
   a.units = static_cast<long long>(cache->B) * a.span * cache->Hkv;
@@ -279,6 +304,40 @@ ra_status ra_paged_decode_attention(const void* q, ra_dtype in_dtype, const ra_p
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int et = cache_code(cache->dtype);
   return cache->D == 128 ? launch_paged_d<128>(a, et, mk, mv, st) : launch_paged_d<64>(a, et, mk, mv, st);
+}
+
+size_t ra_page_select_workspace(int B, int Hkv, int max_pages) {
+  if (B < 1 || Hkv < 1 || max_pages < 1) return static_cast<size_t>(-1);
+  return align256(static_cast<size_t>(B) * Hkv * max_pages * 8);
+}
+
+ra_status ra_page_select(const void* q, ra_dtype in_dtype, const ra_paged_cache* cache, int Tq, int Hq, int n_sel,
+                         int32_t* selected, void* workspace, size_t workspace_bytes, void* stream) {
+  ra_status s = check_batch(cache);
+  if (s != RA_OK) return s;
+  s = check_queries(cache->B, Tq, Hq, cache->Hkv, cache->D);
+  if (s != RA_OK) return s;
+  if (cache->B > 65535 || cache->Hkv > 65535) return RA_ERR_UNSUPPORTED;
+  if (in_dtype != RA_BF16) return in_dtype == RA_F32 ? RA_ERR_UNSUPPORTED : RA_ERR_INVALID_ARG;
+  if (n_sel < page_span(Tq, cache->page_size)) return RA_ERR_INVALID_ARG;
+  if (!q || !aligned16(q) || !cache->key_bounds || !aligned16(cache->key_bounds) || !selected || !aligned4(selected))
+    return RA_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < ra_page_select_workspace(cache->B, cache->Hkv, cache->max_pages))
+    return RA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255) return RA_ERR_INVALID_ARG;
+  SelectArgs a;
+  memset(&a, 0, sizeof(a));
+  a.bt = batch_of(cache, Tq);
+  a.Hq = Hq;
+  a.groups = Hq / cache->Hkv;
+  a.rows = a.groups * Tq;
+  a.n_sel = n_sel;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.bounds = static_cast<const __nv_bfloat16*>(cache->key_bounds);
+  a.keys = static_cast<unsigned long long*>(workspace);
+  a.selected = selected;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cache->D == 128 ? launch_select_d<128>(a, st) : launch_select_d<64>(a, st);
 }
 
 }  // extern "C"

@@ -419,6 +419,35 @@ ra_status ra_paged_decode_attention(const void* q, ra_dtype in_dtype, const ra_p
 size_t ra_paged_decode_workspace(int B, int Tq, int Hq, int Hkv, int D);
 
 /*
+ * ra_page_select - for each sequence and KV head the n_sel pages with the
+ * highest score, for ra_paged_decode_attention's `selected`.
+ *     score(b, g, p) = max over the real query rows of KV head g of
+ *                      sum_d max(q_d lo_d, q_d hi_d)
+ * with lo, hi the page's key_bounds: no key of the page scores higher.  The
+ * sums are taken in 64 bits, so that the choice does not hang on rounding.
+ * The pages that hold new tokens come before all others (so every causal row
+ * sees its own token); of equal scores the lower page comes first.  An infinite
+ * bound counts as 2^128 with its sign; a row whose sum is NaN (of an infinite or
+ * NaN query) does not count.
+ *  q, in_dtype, Tq, Hq   as in ra_paged_decode_attention.
+ *  cache      key_bounds, the table, the lengths and n_pages, page_size, Hkv,
+ *             D are used (as ra_cache_append left them); pages, scales and dtype
+ *             are not.
+ *  n_sel      >= the pages that Tq consecutive tokens can touch,
+ *             1 + ceil((Tq - 1) / page_size).
+ *  selected   device int32 [B, Hkv, n_sel], written: ascending table indices;
+ *             every page, then -1, where a sequence has no more than n_sel.
+ *  workspace  device scratch of ra_page_select_workspace() bytes, 256-byte
+ *             aligned; its contents need no preparation.
+ * B, Hkv <= 65535.  The result does not depend on scheduling.
+ */
+ra_status ra_page_select(const void* q, ra_dtype in_dtype, const ra_paged_cache* cache, int Tq, int Hq, int n_sel,
+                         int32_t* selected, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of ra_page_select ((size_t)-1 when the arguments are invalid). */
+size_t ra_page_select_workspace(int B, int Hkv, int max_pages);
+
+/*
  * ra_ring_attention_backward - gradients of ra_ring_attention.
  * [RA] SOTA-181: ring attention trains models (the backward pass of exact
  * attention); [TR] "What carries the argument": the forward's lse is the

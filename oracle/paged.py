@@ -136,7 +136,9 @@ def select(q, bounds, page_size, table, seq_lens, new_lens, n_sel):
 
     score(b, g, p) = max over the real query rows of KV head g of
     sum_d max(q_d lo_pd, q_d hi_pd); the pages that hold new tokens come before
-    all others; of equal scores the lower page comes first."""
+    all others; of equal scores the lower page comes first.  An infinite bound
+    (an infinite key) counts as 2^128, so that 0 times it is 0."""
+    bounds = np.clip(bounds, -2.0 ** 128, 2.0 ** 128)
     B, Tq, Hq, D = q.shape
     Hkv, ps = bounds.shape[1], page_size
     G = Hq // Hkv

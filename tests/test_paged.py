@@ -124,6 +124,35 @@ def test_paged_decode_workspace(ra):
             ra.ra_paged_decode_workspace(*bad)
 
 
+def select(ra, c, q=FAKE, in_dtype=1, Tq=1, Hq=8, n_sel=4, selected=FAKE, ws=FAKE, ws_bytes=1 << 40):
+    return ra._lib.ra_page_select(q, in_dtype, ctypes.byref(c), Tq, Hq, n_sel, selected, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), 1), (dict(q=FAKE + 8), 1), (dict(in_dtype=0), 2), (dict(in_dtype=3), 1), (dict(Tq=0), 1),
+    (dict(Hq=7), 1), (dict(Hq=2, Tq=65), 2), (dict(n_sel=0), 1), (dict(n_sel=-1), 1),
+    (dict(Tq=2, n_sel=1), 1), (dict(Tq=18, Hq=2, n_sel=2), 1),    # fewer than the new tokens' own pages
+    (dict(selected=None), 1), (dict(selected=FAKE + 2), 1), (dict(ws=None), 3), (dict(ws_bytes=3 * 2 * 10 * 8 - 1), 3),
+    (dict(ws=FAKE + 8), 1)])
+def test_page_select_refuses(ra, kw, status):
+    assert select(ra, cache(ra, key_bounds=FAKE), **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(key_bounds=None), 1), (dict(key_bounds=FAKE + 8), 1), (dict(B=65536), 2), (dict(Hkv=65536), 2),
+    (dict(page_size=24), 2), (dict(D=80), 2), (dict(page_table=None), 1), (dict(seq_lens=FAKE + 2), 1),
+    (dict(n_pages=0), 1)])
+def test_page_select_refuses_a_bad_cache(ra, kw, status):
+    c = dict(dict(key_bounds=FAKE), **kw)
+    assert select(ra, cache(ra, **c), Hq=8 if kw.get("Hkv", 2) == 2 else 65536) == status
+
+
+def test_page_select_workspace(ra):
+    assert ra.ra_page_select_workspace(3, 2, 10) >= 3 * 2 * 10 * 8
+    with pytest.raises(ra.RAError):
+        ra.ra_page_select_workspace(1, 0, 10)
+
+
 # ------------------------------------------------------------- oracle pins
 
 def test_e4m3_grid_is_the_types():
