@@ -73,25 +73,7 @@ ra_status launch_read_t(const ReadArgs& a, int et, unsigned grid, cudaStream_t s
   return cuda_status(cudaGetLastError());
 }
 
-// Pages of one tensor as rows of D values, box = 16 or 32 rows of one column
-// half (128 bytes; whole rows of an 8-bit cache), swizzled for the fragment loads.
-bool make_page_map(CUtensorMap* m, const void* ptr, const ra_paged_cache* c) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  const int elem = c->dtype == RA_BF16 ? 2 : 1;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c->D),
-                              static_cast<cuuint64_t>(c->n_pages) * c->Hkv * c->page_size};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(c->D) * elem};
-  const cuuint32_t cols = static_cast<cuuint32_t>(c->D * elem > 128 ? 128 / elem : c->D);
-  const cuuint32_t box[2] = {cols, c->page_size == 16 ? 16u : 32u};
-  const cuuint32_t es[2] = {1, 1};
-  return enc(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-             const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             cols * elem == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-constexpr int kPgMinTiles = 4;  // shortest run of a team, in tiles of 32 keys
+constexpr int kPgMinRun = kPgPairCost + 2;  // shortest run of a team, in units of the line
 
 struct PagedPlan {
   int rows, R, teams;  // query rows per KV head, warps per team, teams of a full grid
@@ -110,7 +92,7 @@ PagedPlan paged_plan(int B, int Tq, int Hq, int Hkv, int D) {
   PagedPlan p;
   p.rows = (Hq / Hkv) * Tq;
   p.R = p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
-  p.teams = sm_count() * (kPgWarps / p.R);
+  p.teams = sm_count() * (p.R == 1 ? 15 : 11 / p.R);  // most consumer warps of any cache type
   p.part_o = 0;
   p.part_ml = align256(static_cast<size_t>(p.teams) * 2 * p.rows * D * 4);
   p.cut = align256(p.part_ml + static_cast<size_t>(p.teams) * 2 * p.rows * 8);
@@ -118,56 +100,61 @@ PagedPlan paged_plan(int B, int Tq, int Hq, int Hkv, int D) {
   return p;
 }
 
-template <int D, int WPR>
+template <int D, int WPR, int NW>
 ra_status launch_paged_combine(const PagedArgs& a, int teams, cudaStream_t st) {
   const long long rows = static_cast<long long>(a.bt.B) * a.bt.Hkv * a.rows;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 8 / WPR - 1) / (8 / WPR)), 1, 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + NW / WPR - 1) / (NW / WPR)), 1, 1);
+  cfg.blockDim = dim3(32 * NW, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, WPR>, a, teams));
+  return cuda_status(cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, WPR, NW>, a, teams));
 }
 
-template <int D, int ET>
-ra_status launch_paged_t(PagedArgs a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
-  using SL = PgSmem<D, ET>;
+template <int D, int ET, int NB>
+ra_status launch_paged_t(const PagedArgs& a, cudaStream_t st) {
+  using SL = PgSmem<D, ET, NB>;
   static int attr_set[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 64 || !attr_set[dev]) {
-    if (cudaFuncSetAttribute(paged_partial_kernel<D, ET>, cudaFuncAttributeMaxDynamicSharedMemorySize, SL::kBytes) !=
-        cudaSuccess)
+    if (cudaFuncSetAttribute(paged_partial_kernel<D, ET, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             SL::kBytes) != cudaSuccess)
       return RA_ERR_CUDA;
     if (dev < 64) attr_set[dev] = 1;
   }
-  a.slots = a.R * kPgRing / SL::kItem;
-  if (a.slots > kPgSlots * a.R) a.slots = kPgSlots * a.R;
   // the longest line that the table (or the selection) allows
   const long long pages = a.selected && a.n_sel < a.bt.max_pages ? a.n_sel : a.bt.max_pages;
   const long long tiles = ((pages << a.bt.page_shift) + kPgKeys - 1) / kPgKeys;
-  const long long line = tiles * a.bt.B * a.bt.Hkv;
-  const long long runs = (line + a.min_tiles - 1) / a.min_tiles;
+  const long long line = (tiles + kPgPairCost) * a.bt.B * a.bt.Hkv;
+  const long long runs = (line + a.min_run - 1) / a.min_run;
   const int grid = static_cast<int>(runs < sm_count() ? runs : sm_count());
-  paged_partial_kernel<D, ET><<<grid, kPgThreads, SL::kBytes, st>>>(mk, mv, a);
+  paged_partial_kernel<D, ET, NB><<<grid, SL::kThreads, SL::kBytes, st>>>(a);
   const ra_status s = cuda_status(cudaGetLastError());
   if (s != RA_OK) return s;
-  // a row's parts: 8 warps where rows are few, one where they alone fill the GPU
+  // a row's parts: 32 warps where the rows are few, one where they alone fill the GPU
   const long long rows = static_cast<long long>(a.bt.B) * a.bt.Hkv * a.rows;
-  const int teams = grid * (kPgWarps / a.R);
-  return rows <= 2048 ? launch_paged_combine<D, 8>(a, teams, st) : launch_paged_combine<D, 1>(a, teams, st);
+  const int teams = grid * (SL::kWarps / a.R);
+  if (rows <= 2 * sm_count()) return launch_paged_combine<D, 32, 32>(a, teams, st);
+  if (rows <= 16 * sm_count()) return launch_paged_combine<D, 8, 8>(a, teams, st);
+  return launch_paged_combine<D, 1, 8>(a, teams, st);
+}
+
+template <int D, int ET>
+ra_status launch_paged_e(const PagedArgs& a, cudaStream_t st) {
+  return a.rows <= 8 ? launch_paged_t<D, ET, 1>(a, st) : launch_paged_t<D, ET, 2>(a, st);
 }
 
 template <int D>
-ra_status launch_paged_d(const PagedArgs& a, int et, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
-  if (et == kCacheBf16) return launch_paged_t<D, kCacheBf16>(a, mk, mv, st);
-  if (et == kCacheI8) return launch_paged_t<D, kCacheI8>(a, mk, mv, st);
-  return launch_paged_t<D, kCacheE4M3>(a, mk, mv, st);
+ra_status launch_paged_d(const PagedArgs& a, int et, cudaStream_t st) {
+  if (et == kCacheBf16) return launch_paged_e<D, kCacheBf16>(a, st);
+  if (et == kCacheI8) return launch_paged_e<D, kCacheI8>(a, st);
+  return launch_paged_e<D, kCacheE4M3>(a, st);
 }
 
 // Most pages that T consecutive tokens touch.
@@ -277,8 +264,6 @@ ra_status ra_paged_decode_attention(const void* q, ra_dtype in_dtype, const ra_p
   const PagedPlan p = paged_plan(cache->B, Tq, Hq, cache->Hkv, cache->D);
   if (!workspace || workspace_bytes < p.total) return RA_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return RA_ERR_INVALID_ARG;
-  CUtensorMap mk, mv;
-  if (!make_page_map(&mk, cache->k_pages, cache) || !make_page_map(&mv, cache->v_pages, cache)) return RA_ERR_CUDA;
   PagedArgs a;
   memset(&a, 0, sizeof(a));
   a.bt = batch_of(cache, Tq);
@@ -287,11 +272,13 @@ ra_status ra_paged_decode_attention(const void* q, ra_dtype in_dtype, const ra_p
   a.rows = p.rows;
   a.causal = causal != 0;
   a.R = p.R;
-  a.min_tiles = kPgMinTiles;
+  a.min_run = kPgMinRun;
   a.n_sel = n_sel;
   a.selected = selected;
   a.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(cache->D)));
   a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k_pages = cache->k_pages;
+  a.v_pages = cache->v_pages;
   a.k_scales = cache->k_scales;
   a.v_scales = cache->v_scales;
   char* ws = static_cast<char*>(workspace);
@@ -303,7 +290,7 @@ ra_status ra_paged_decode_attention(const void* q, ra_dtype in_dtype, const ra_p
   a.lse = lse;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int et = cache_code(cache->dtype);
-  return cache->D == 128 ? launch_paged_d<128>(a, et, mk, mv, st) : launch_paged_d<64>(a, et, mk, mv, st);
+  return cache->D == 128 ? launch_paged_d<128>(a, et, st) : launch_paged_d<64>(a, et, st);
 }
 
 size_t ra_page_select_workspace(int B, int Hkv, int max_pages) {

@@ -6,38 +6,57 @@
 // their log-sum-exp.  Here a chunk is whatever run of the cache one team of
 // warps walks, and it may begin and end anywhere in a sequence.
 //
-// Mathematics, per query row (s = 1 / sqrt(D), everything in fp32):
-//     x_j = s (q . k_j),  m = max x_j,  l = sum e^(x_j - m),  o = sum e^(x_j - m) v_j,
-//     out = o / l,  lse = m + ln l,
-// with the running (m, l, o) rescaled whenever m grows.  For an 8-bit cache the
-// codes are turned into bf16 (exactly: 8 significant bits at most) and the
-// scales enter as factors: x_j = (s ks_j) (q . code_j), and e^(x_j - m) vs_j is the
-// weight of v's codes.  The weights go to the tensor core as two bf16 terms
-// (their rounding and what it left: 16 bits, an error of at most 2^-17), or
-// three for an fp32 output (24 bits): a single bf16 weight (2^-9) would cost
-// as much accuracy as the output's own rounding.
+// Mathematics, per query row (c = log2(e) / sqrt(D), everything in fp32), of an
+// 8-bit cache with key and value scales ks_j, vs_j (both 1 for bf16):
+//     x_j = c ks_j (q . k_j),   w_j = vs_j 2^(x_j - E),
+//     l = sum 2^(x_j - E),   o = sum w_j v_j,   out = o / l,   lse = ln 2 (E + log2 l)
+// with k_j, v_j the codes as they are stored.  E is any reference for which no
+// term overflows: out and lse do not depend on it.  It starts at the first
+// tile's max (x_j + log2 vs_j), which makes the largest w_j 1, and is raised, with
+// l and o rescaled, only when a w_j passes kPgLazy.  So most tiles need no
+// maximum across lanes at all: each lane looks at its own terms, and one vote
+// says that none is too large.
+//
+// The weights w_j go to the tensor core as two 16-bit terms, the leading bits
+// and the rounded remainder, or three for an fp32 output: with bf16 (cache in
+// bf16) 2^-17 or 2^-24 relative, with f16 (8-bit cache) 2^-22 relative and
+// 2^-25 of the largest w.  One rounded term (2^-9 for bf16) would cost as much
+// accuracy as the output's own rounding.  8-bit codes are turned into f16, which
+// holds them exactly; the queries then go in as f16 too, scaled by a power of two
+// that brings the warp's largest to 2^14 (bf16's 8 bits fit, and what falls
+// under f16's range is below 2^-38 of the largest).
 //
 // Bound by HBM: a cached element meets the groups * Tq (<= 64) query rows of its
-// KV head and is used once.  So the cache is streamed once by TMA through
-// rings of shared memory, and the products are mma.sync on tiles of 16 rows.
+// KV head and is used once.  So the cache is streamed once, through rings of
+// shared memory, by 16-byte asynchronous copies: a page of one head may be as
+// small as 1 KB and the tile's scales are 128 bytes, and a TMA copy costs the
+// same to issue whatever its size (with TMA, 16-key pages of int8 took 111 us
+// where 64-key ones took 88; eight sequences of 9k to 24k keys, 8 heads, 128
+// columns).  The products are mma.sync m16n8k16 with the keys
+// (scores) or the columns (output) on the 16 side and the query rows on the 8
+// side: up to 8 rows, the usual single token, cost half of what rows on the 16
+// side would, in products, in exponentials and in accumulator registers.
+// (tcgen05 takes 128 by at least 16 and would add a pass through tensor memory.)
 //
 // Work split: the cache of all (sequence, KV head) pairs, cut into tiles of 32
-// keys, is one line of tiles (sequence-major, then head, then position).  The
-// lengths are on the device, so each team works out the line's length from
-// them and takes an equal run of it; runs cross sequence borders, so a batch
-// of one 100k and many short sequences is as even as a uniform one, with
-// one grid shape for all lengths (a captured graph replays with new ones).
-// A team's run covers whole (sequence, head) pairs, written out directly, and
-// at most two cut ones (its first and last), left as (m, l, o) in the workspace
-// for the combine kernel, which knows each cut pair from a record that the
-// team holding its first tile writes.
+// keys, is one line of tiles (sequence-major, then head, then position) in
+// which each pair also takes kPgPairCost units for its start and end.  The
+// lengths are on the device, so the teams work out the line's length from them
+// and take equal runs of it; runs cross pair borders, so a batch of one 100k
+// and many short sequences is as even as a uniform one, with one grid shape
+// for all lengths (a captured graph replays with new ones).  A team's run
+// covers whole pairs, written out directly, and at most two cut ones (its first
+// and last), left as (E, l, o) in the workspace for the combine kernel, which
+// knows each cut pair from a record of its first and last team.
 //
-// A team is one warp for up to 16 query rows, 2 or 4 warps for up to 32 or 64
-// (each warp one 16-row tile; the team shares its ring).  The warps of a team
-// never meet at a barrier with other teams: softmax statistics are per warp
-// (four lanes to a row), P goes from the score accumulators to the next
-// product's operand registers without touching shared memory.
+// A CTA has one walker warp, whose lane t walks the run of team t, looks up pages
+// and queues the tiles in shared memory, and kWarps consumer warps, which copy
+// and compute them.  A team is one consumer warp for up to 8 (NB = 1) or 16
+// (NB = 2) query rows, 2 or 4 warps (NB = 2) for up to 32 or 64, each with 16 of
+// the rows and all sharing the team's ring.  Teams never meet at a barrier.
 #pragma once
+
+#include <type_traits>
 
 #include "attn_fwd.cuh"
 #include "decode.cuh"
@@ -45,92 +64,164 @@
 
 namespace ra {
 
-constexpr int kPgWarps = 8;
-constexpr int kPgThreads = 32 * kPgWarps;
-constexpr int kPgKeys = 32;       // keys of a tile
-constexpr int kPgRing = 24576;    // ring bytes per warp
-constexpr int kPgSlots = 8;       // ring items per warp, at most
-constexpr int kPgNone = 0x7fffff00;  // position of a key that no row sees
+constexpr int kPgKeys = 32;         // keys of a tile
+constexpr int kPgQueue = 8;         // tiles queued for a team
+constexpr int kPgSlots = 8;         // ring items per warp, at most
+constexpr int kPgPairCost = 3;      // a pair's start and end, in tiles
+constexpr float kPgLazy = 1024.f;   // a weight above this moves the reference E (f16 ends at 65504)
+constexpr int kPgNone = 0x7fffff00; // position of a key that no row sees
 
 struct PagedArgs {
   PagedBatch bt;  // T = Tq
   int Hq, groups, rows, causal;
-  int R;         // warps per team: 16-row tiles of the query rows of one KV head
-  int slots;     // ring items per team
-  int min_tiles; // a team's run is at least this long
+  int R;         // warps per team
+  int min_run;   // a team's run is at least this long
   int n_sel;
   const int* selected;  // [B][Hkv][n_sel] or null
   float scale_log2;
   const __nv_bfloat16* q;  // [B][Tq][Hq][D]
+  const void* k_pages;
+  const void* v_pages;
   const float* k_scales;
   const float* v_scales;
   float* part_o;    // [teams][2][rows][D]
-  float2* part_ml;  // [teams][2][rows]: m (log2 units), l
+  float2* part_ml;  // [teams][2][rows]: E (log2 units), l
   int2* cut;        // [B * Hkv]: first and last team of a cut pair; first < 0: not cut
   void* out;        // [B][Tq][Hq][D]
   int out_bf16;
   float* lse;
 };
 
-template <int D, int ET>
+// Shared memory and the shape of a CTA.  bf16: 8 consumer warps with rings of
+// 24 KB keep the copies in flight that HBM needs.  An 8-bit tile has half the
+// bytes and a conversion of its codes besides, so instruction issue is what
+// must be fed: 15 warps of 8 rows (128 registers), 11 of 16 rows (168: the
+// output accumulators alone take 64).  With the producer that is a multiple of
+// four warps, which the register file is shared out by.
+template <int D, int ET, int NB>
 struct PgSmem {
+  static constexpr int kWarps = ET == kCacheBf16 ? 8 : NB == 1 ? 15 : 11;
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kRing = ET == kCacheBf16 ? 24576 : NB == 1 ? 12288 : 16384;  // bytes per warp
   static constexpr int kElem = ET == kCacheBf16 ? 2 : 1;
   static constexpr int kItem = kPgKeys * D * kElem;  // one tile of K or of V
-  static constexpr int kRowBytes = D * kElem < 128 ? D * kElem : 128;
-  static constexpr int kScale = kPgWarps * kPgRing;  // fp32 [64 slots][32]
-  static constexpr int kMeta = kScale + kPgWarps * kPgSlots * kPgKeys * 4;
-  static constexpr int kFull = kMeta + kPgWarps * kPgSlots * 8;
-  static constexpr int kEmpty = kFull + kPgWarps * kPgSlots * 8;
-  static constexpr int kAbort = kEmpty + kPgWarps * kPgSlots * 8;
-  static constexpr int kBytes = kAbort + 16 + 1024;  // + slack to align the base to 1024
+  static constexpr int kSlots = kRing / kItem < kPgSlots ? kRing / kItem : kPgSlots;  // per warp
+  static constexpr int kRow = D * kElem;  // bytes of a cached row
+  static constexpr int kScale = kWarps * kRing;                          // fp32 [slots][32]
+  static constexpr int kMeta = kScale + (ET == kCacheBf16 ? 0 : kWarps * kSlots * kPgKeys * 4);
+  static constexpr int kFull = kMeta + kWarps * kPgQueue * 32;           // barriers of the ring items
+  static constexpr int kEmpty = kFull + kWarps * kSlots * 8;
+  static constexpr int kQFull = kEmpty + kWarps * kSlots * 8;            // and of the queue entries
+  static constexpr int kQEmpty = kQFull + kWarps * kPgQueue * 8;
+  static constexpr int kAbort = kQEmpty + kWarps * kPgQueue * 8;
+  static constexpr int kBytes = kAbort + 16 + 256;  // + slack to align the base to 256
 };
 
-// Byte offset of the 16-byte chunk c of key j in a tile that TMA wrote with
-// 128-byte swizzle (64-byte for rows of 64 bytes); a bf16 tile of D = 128 is two
-// halves of 64 columns.
-template <int D, int ET>
+// Ring items of a team: the loads run ahead of the tile in work by this many,
+// which the queue has to cover.
+template <typename SL>
+__device__ __forceinline__ int pg_slots(int R) {
+  return min(SL::kSlots * R, 2 * (kPgQueue - 2));
+}
+
+// A queued tile: the cache rows and the positions of the first key of each 16,
+// the pair, its lengths, and these flags.
+enum { kPgFirst = 1, kPgLast = 2, kPgWhole = 4, kPgOwner = 8, kPgStop = 16 };
+struct alignas(16) PgTile {
+  int r0, r1, p0, p1;
+  int b, h, len;
+  int fresh_flags;  // new tokens << 8 | flags
+};
+
+// Byte offset of the 16-byte chunk c of key j in a tile of rows of ROW bytes:
+// chunks permuted within 128 bytes so that eight keys' chunks lie in eight
+// different bank groups.
+template <int ROW>
 __device__ __forceinline__ uint32_t pg_off(int j, int c) {
-  if constexpr (PgSmem<D, ET>::kRowBytes == 128)
-    return (c >> 3) * (kPgKeys * 128) + j * 128 + (((c & 7) ^ (j & 7)) << 4);
-  else
-    return j * 64 + ((c ^ ((j >> 1) & 3)) << 4);
+  return j * ROW + ((c ^ (ROW >= 128 ? j & 7 : (j >> 1) & 3)) << 4);
 }
 
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, int c0, int c1, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(bar)
-      : "memory");
-}
-
-// Untiled copy of a multiple of 16 bytes, both ends 16-byte aligned; no multicast.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src))
                : "memory");
 }
 
-__device__ __forceinline__ uint32_t bf16x2_sub(uint32_t a, uint32_t b) {
-  __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
-  return *reinterpret_cast<uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
-  __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
-  return *reinterpret_cast<uint32_t*>(&r);
+// Arrives on `bar` (once per thread) when this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// The codes in bytes 0 and 2 of w as two bf16 values, exactly.
-//   int8: 128 + (low 7 bits) and 128 + 128 (sign bit) are bf16 bit patterns
-//   (0x4300 | bits); their difference is the signed value.
-//   e4m3: sign, exponent and mantissa moved into bf16's fields, times
-//   2^(127 - 7) (0x7b80), which covers the subnormal codes too.
+__device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// D (16x8 fp32) += A (16x16, row-major) * B (16x8, column-major), operands bf16
+// for a bf16 cache, f16 for an 8-bit one.
 template <int ET>
-__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t w) {
-  if constexpr (ET == kCacheI8)
-    return bf16x2_sub((w & 0x007f007fu) | 0x43004300u, (w & 0x00800080u) | 0x43004300u);
+__device__ __forceinline__ void pg_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (ET == kCacheBf16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    return bf16x2_mul(((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u), 0x7b807b80u);
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8x8 matrix of 16-bit values held two to a lane (row lane / 4,
+// columns 2 (lane % 4), + 1).
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The codes in bytes 0 and 2 of w as two f16 values, exactly: 0x6400 | u is the
+// f16 1024 + u, so with the sign bit flipped (u = code + 128) and 1152 taken
+// away the signed code is left.
+__device__ __forceinline__ uint32_t i8_to_f16(uint32_t w) {
+  uint32_t r;  // lop3 0x6a: (w & 0x00ff00ff) ^ 0x64806480
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(w), "r"(0x00ff00ffu), "r"(0x64806480u));
+  asm("add.rn.f16x2 %0, %0, %1;" : "+r"(r) : "r"(0xe480e480u));
+  return r;
+}
+
+// The e4m3 codes in bytes 0 and 1 (HALF = 0) or 2 and 3 of w as two f16 values.
+template <int HALF>
+__device__ __forceinline__ uint32_t e4m3_to_f16(uint32_t w) {
+  uint32_t r;
+  if constexpr (HALF == 0)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+  else
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+// A pair of weights as 16-bit pairs of the operand type: the leading bits (cut
+// off, so that the remainder is exact), then the rounded remainder, and for a
+// bf16 operand and an fp32 output what that left (f16 has 22 bits by then).
+template <int ET>
+__device__ __forceinline__ void split_pair(float x, float y, bool three, uint32_t (&t)[3]) {
+  constexpr uint32_t kCut = ET == kCacheBf16 ? 0xffff0000u : 0xffffe000u;  // 8 or 11 bits
+  const float xh = __uint_as_float(__float_as_uint(x) & kCut), yh = __uint_as_float(__float_as_uint(y) & kCut);
+  const float xr = x - xh, yr = y - yh;
+  t[2] = 0u;
+  if constexpr (ET == kCacheBf16) {
+    t[0] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+    t[1] = pack_bf16x2(xr, yr);
+    if (three)
+      t[2] = pack_bf16x2(xr - __uint_as_float(t[1] << 16), yr - __uint_as_float(t[1] & 0xffff0000u));
+  } else {
+    t[0] = pack_f16x2(xh, yh);
+    t[1] = pack_f16x2(xr, yr);
+  }
 }
 
 // Tiles of one (sequence, KV head) pair.
@@ -140,75 +231,17 @@ __device__ __forceinline__ int pg_tiles(const PagedArgs& a, int len) {
   return ((min(a.n_sel, pages) << a.bt.page_shift) + kPgKeys - 1) / kPgKeys;
 }
 
-// A place on the line of tiles.
-struct PgWalk {
-  int b, h, t, nt;
-  SeqLen s;
-};
-
-// First sequence at or behind b that has tiles (whole warp).
-__device__ __forceinline__ void pg_seek(const PagedArgs& a, PgWalk& w, int b, int lane) {
-  for (; b < a.bt.B; b += 32) {
-    const int n = b + lane < a.bt.B ? a.bt.seq_lens[b + lane] : 0;
-    const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
-    if (some) {
-      b += __ffs(some) - 1;
-      break;
-    }
-  }
-  w.b = min(b, a.bt.B);
-  w.h = w.t = 0;
-  w.nt = 0;
-  if (w.b < a.bt.B) {
-    w.s = seq_len_of(a.bt, w.b);
-    w.nt = pg_tiles(a, w.s.len);
-  }
+// Units of the line that a sequence takes: its pairs' tiles and costs.
+__device__ __forceinline__ long long pg_units(const PagedArgs& a, int len) {
+  const int n = pg_tiles(a, len);
+  return n > 0 ? static_cast<long long>(n + kPgPairCost) * a.bt.Hkv : 0;
 }
 
-__device__ __forceinline__ void pg_next(const PagedArgs& a, PgWalk& w, int lane) {
-  if (++w.t < w.nt) return;
-  w.t = 0;
-  if (++w.h < a.bt.Hkv) return;
-  pg_seek(a, w, w.b + 1, lane);
+// Element of the output at column d of a row.
+__device__ __forceinline__ void pg_store1(const PagedArgs& a, long long row, int D, int d, float x) {
+  if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(x);
+  else static_cast<float*>(a.out)[row * D + d] = x;
 }
-
-// Tiles of the whole line (whole warp).
-__device__ __forceinline__ long long pg_total(const PagedArgs& a, int lane) {
-  long long n = 0;
-  for (int b = lane; b < a.bt.B; b += 32) n += pg_tiles(a, seq_len_of(a.bt, b).len);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n * a.bt.Hkv;
-}
-
-// The place of tile f of the line, f below pg_total (whole warp).
-__device__ __forceinline__ void pg_locate(const PagedArgs& a, long long f, PgWalk& w, int lane) {
-  long long before = 0;
-  for (int b0 = 0; b0 < a.bt.B; b0 += 32) {
-    const int b = b0 + lane;
-    const long long mine = b < a.bt.B ? static_cast<long long>(pg_tiles(a, seq_len_of(a.bt, b).len)) * a.bt.Hkv : 0;
-    long long upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, before + upto > f);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      const long long rel = f - before - __shfl_sync(0xffffffffu, upto - mine, l);
-      w.b = b0 + l;
-      w.s = seq_len_of(a.bt, w.b);
-      w.nt = pg_tiles(a, w.s.len);
-      w.h = static_cast<int>(rel / w.nt);
-      w.t = static_cast<int>(rel % w.nt);
-      return;
-    }
-    before += __shfl_sync(0xffffffffu, upto, 31);
-  }
-}
-
-// One output element pair or quad at columns d.. of a row.
 __device__ __forceinline__ void pg_store2(const PagedArgs& a, long long row, int D, int d, float x, float y) {
   if (a.out_bf16)
     *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + row * D + d) = pack_bf16x2(x, y);
@@ -216,335 +249,544 @@ __device__ __forceinline__ void pg_store2(const PagedArgs& a, long long row, int
     *reinterpret_cast<float2*>(static_cast<float*>(a.out) + row * D + d) = make_float2(x, y);
 }
 
-template <int D, int ET>
-__global__ void __launch_bounds__(kPgThreads, 1)
-    paged_partial_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                         const __grid_constant__ PagedArgs a) {
-  using SL = PgSmem<D, ET>;
-  constexpr int NT = D / 8;    // n8 blocks of the output
-  constexpr int KS = D / 16;   // k16 steps of the score product
+// ------------------------------------------------------------------ walker
+
+// The walker warp: lane t < teams walks the run of team t.  In every round the
+// lanes whose queue has room post one tile.  Page numbers are loaded when a
+// tile is reached and used in the round that posts it, so their latency
+// overlaps the rounds between.
+template <int D, int ET, int NB>
+__device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volatile int* abort_flag) {
+  using SL = PgSmem<D, ET, NB>;
+  const int lane = threadIdx.x & 31;
+  const int teams = SL::kWarps / a.R;
+  const uint32_t sb = smem_u32(smem);
+  const uint32_t qfull = sb + SL::kQFull + 8u * kPgQueue * lane, qempty = sb + SL::kQEmpty + 8u * kPgQueue * lane;
+  PgTile* queue = reinterpret_cast<PgTile*>(smem + SL::kMeta) + kPgQueue * lane;
+  const int ps = 1 << a.bt.page_shift;
+
+  // the line and this lane's run [f0, f1) of it
+  long long total = 0;
+  for (int b = lane; b < a.bt.B; b += 32) total += pg_units(a, seq_len_of(a.bt, b).len);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const long long U = static_cast<long long>(gridDim.x) * teams;
+  const long long u = static_cast<long long>(lane) * gridDim.x + blockIdx.x;
+  long long run = (total + U - 1) / U;
+  if (run < a.min_run) run = a.min_run;
+  const long long f0 = u * run, f1 = min(f0 + run, total);
+  bool work = lane < teams && f0 < f1;
+  // its place: sequence b (starting at unit `start` of the line)
+  int b = 0;
+  long long start = 0;
+  {
+    long long before = 0;
+    bool found = false;
+    for (int b0 = 0; b0 < a.bt.B; b0 += 32) {
+      long long upto = b0 + lane < a.bt.B ? pg_units(a, seq_len_of(a.bt, b0 + lane).len) : 0;
+      const long long mine = upto;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const int n = min(32, a.bt.B - b0);
+      for (int i = 0; i < n; ++i) {
+        const long long e = before + __shfl_sync(0xffffffffu, upto, i);
+        const long long s = e - __shfl_sync(0xffffffffu, mine, i);
+        if (work && !found && f0 < e) {
+          found = true;
+          b = b0 + i;
+          start = s;
+        }
+      }
+      before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
+  SeqLen s = {0, 0};
+  int nt = 0, h = 0, t = 0;
+  long long pair0 = 0;  // the pair's first unit on the line
+  if (work) {
+    s = seq_len_of(a.bt, b);
+    nt = pg_tiles(a, s.len);
+    const long long rel = f0 - start;
+    h = static_cast<int>(rel / (nt + kPgPairCost));
+    pair0 = start + static_cast<long long>(h) * (nt + kPgPairCost);
+    t = max(static_cast<int>(f0 - pair0) - kPgPairCost, 0);
+  }
+  // the next tile with work at or behind (b, h, t); work = false behind the run's end
+  auto settle = [&]() {
+    while (work) {
+      if (pair0 + kPgPairCost + t >= f1) work = false;  // the rest of the line is other teams'
+      else if (t < nt) break;
+      else {
+        pair0 += nt + kPgPairCost;
+        t = 0;
+        if (++h == a.bt.Hkv) {
+          h = 0;
+          do {
+            ++b;
+            s = b < a.bt.B ? seq_len_of(a.bt, b) : SeqLen{0, 0};
+            nt = pg_tiles(a, s.len);
+          } while (b < a.bt.B && nt == 0);
+          if (b >= a.bt.B) work = false;
+        }
+      }
+    }
+  };
+  // Table index of the 16 keys from 16 u of the pair; -1 for none.
+  auto logical_of = [&](int unit) -> int {
+    const long long key = 16LL * unit;
+    if (a.selected == nullptr) return key < s.len ? static_cast<int>(key >> a.bt.page_shift) : -1;
+    const int pages = (s.len + ps - 1) >> a.bt.page_shift;
+    const int idx = static_cast<int>(key >> a.bt.page_shift);
+    if (idx >= min(a.n_sel, pages)) return -1;
+    const int* sel = a.selected + (static_cast<long long>(b) * a.bt.Hkv + h) * a.n_sel;
+    const int x = sel[idx], prev = idx > 0 ? sel[idx - 1] : -1;
+    if (x == -1) return -1;
+    if (x < 0 || x >= pages || x <= prev) {
+      set_status(RA_ERR_DEVICE_BOUNDS);
+      return -1;
+    }
+    return x;
+  };
+  // the tile's one or two pages: table indices and what the table holds there
+  int lg0 = -1, lg1 = -1, pg0 = 0, pg1 = 0;
+  auto look_up = [&]() {
+    const int* row = a.bt.page_table + static_cast<long long>(b) * a.bt.max_pages;
+    lg0 = logical_of(2 * t);
+    if (lg0 >= 0) pg0 = row[lg0];
+    if (ps == 16) {
+      lg1 = logical_of(2 * t + 1);
+      if (lg1 >= 0) pg1 = row[lg1];
+    }
+  };
+  settle();
+  if (work) look_up();
+
+  bool first = true, stopped = lane >= teams;
+  int posted = 0, slot = 0;
+  uint32_t phase = 0;
+  long long t0 = clock64();
+  while (true) {
+    const bool go = !stopped && (posted < kPgQueue || mbar_test_wait(qempty + 8u * slot, phase ^ 1u));
+    if (go) {
+      PgTile m;
+      m.r0 = m.r1 = 0;
+      m.p0 = m.p1 = kPgNone;
+      m.b = b;
+      m.h = h;
+      m.len = s.len;
+      const int fresh = s.fresh;
+      int flags = kPgStop;  // the run's end
+      if (work) {
+        auto place = [&](int lg, int pg, int key, int& r, int& p) {
+          if (lg < 0) return;
+          if (pg < 0 || pg >= a.bt.n_pages) {
+            set_status(RA_ERR_DEVICE_BOUNDS);
+            return;
+          }
+          r = ((pg * a.bt.Hkv + h) << a.bt.page_shift) + (key & (ps - 1));
+          p = (lg << a.bt.page_shift) + (key & (ps - 1));
+        };
+        place(lg0, pg0, 32 * t, m.r0, m.p0);
+        if (ps == 16) {
+          place(lg1, pg1, 32 * t + 16, m.r1, m.p1);
+        } else if (m.p0 != kPgNone) {
+          m.r1 = m.r0 + 16;
+          m.p1 = m.p0 + 16;
+        }
+        const bool owner = pair0 + kPgPairCost >= f0;
+        const bool last = t + 1 == nt || pair0 + kPgPairCost + t + 1 >= f1;
+        flags = (first ? kPgFirst : 0) | (last ? kPgLast : 0) | (owner && t + 1 == nt ? kPgWhole : 0) | (owner ? kPgOwner : 0);
+        if (first && owner) {  // the pair's record: cut, if its last tile is another team's
+          const long long ul = (pair0 + kPgPairCost + nt - 1) / run;
+          a.cut[static_cast<long long>(b) * a.bt.Hkv + h] =
+              ul == u ? make_int2(-1, -1) : make_int2(static_cast<int>(u), static_cast<int>(ul));
+        }
+        first = last;
+        ++t;
+        settle();
+      } else {
+        stopped = true;
+      }
+      m.fresh_flags = (fresh << 8) | flags;
+      queue[slot] = m;
+      mbar_arrive(qfull + 8u * slot);
+      ++posted;
+      if (++slot == kPgQueue) {
+        slot = 0;
+        phase ^= 1u;
+      }
+      if (work) look_up();
+    }
+    if (__all_sync(0xffffffffu, stopped)) return;
+    if (__any_sync(0xffffffffu, go)) {
+      t0 = clock64();
+      continue;
+    }
+    if (*abort_flag || grid_timed_out()) return;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      set_status(RA_ERR_TIMEOUT);
+      *abort_flag = 1;
+      return;
+    }
+    __nanosleep(500);
+  }
+}
+
+// ---------------------------------------------------------------- consumers
+
+template <int D, int ET, int NB>
+__global__ void __launch_bounds__(PgSmem<D, ET, NB>::kThreads, 1)
+    paged_partial_kernel(const __grid_constant__ PagedArgs a) {
+  using SL = PgSmem<D, ET, NB>;
+  constexpr int KS = D / 16;  // k16 steps of the score product, and 16-column blocks of the output
+  constexpr int NR = 2 * NB;  // query rows of a lane: 8 nb + 2 (lane % 4), + 1
+  constexpr int ROW = SL::kRow;
   extern __shared__ uint8_t pg_raw[];
-  uint8_t* smem = pg_raw + ((1024u - (smem_u32(pg_raw) & 1023u)) & 1023u);
+  uint8_t* smem = pg_raw + ((256u - (smem_u32(pg_raw) & 255u)) & 255u);
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int gr = lane >> 2, qd = lane & 3;  // fragment row and column pair of this lane
-  const int teams = kPgWarps / a.R, team = warp / a.R, rt = warp % a.R;
-  const bool leader = rt == 0;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SL::kAbort);
-  const int slots = a.slots;
-  const uint32_t ring = sb + team * a.R * kPgRing;
-  const int slot0 = team * slots;  // this team's first barrier, scale row and meta entry
-  const uint32_t full = sb + SL::kFull + 8u * slot0, empty = sb + SL::kEmpty + 8u * slot0;
-  int2* meta = reinterpret_cast<int2*>(smem + SL::kMeta) + slot0;
+  const int teams = SL::kWarps / a.R, slots = pg_slots<SL>(a.R);
 
   // the combine kernel may be brought onto the SMs; it waits for this grid's end itself
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid == 0) {
-    *abort_flag = grid_timed_out() ? 1 : 0;
-    for (int i = 0; i < teams * slots; ++i) {
-      mbar_init(sb + SL::kFull + 8u * i, 1);
-      mbar_init(sb + SL::kEmpty + 8u * i, a.R);
-    }
-    fence_mbar_init();
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
+  if (tid == 32 * SL::kWarps) *abort_flag = grid_timed_out() ? 1 : 0;
+  for (int i = tid; i < teams * slots; i += SL::kThreads) {
+    mbar_init(sb + SL::kFull + 8u * i, 32 * a.R);  // every thread of the team
+    mbar_init(sb + SL::kEmpty + 8u * i, a.R);
   }
+  for (int i = tid; i < teams * kPgQueue; i += SL::kThreads) {
+    mbar_init(sb + SL::kQFull + 8u * i, 1);
+    mbar_init(sb + SL::kQEmpty + 8u * i, a.R);
+  }
+  fence_mbar_init();
   __syncthreads();
   if (*abort_flag) return;
+  if (warp == SL::kWarps) {
+    pg_walk<D, ET, NB>(a, smem, abort_flag);
+    return;
+  }
 
   // sequences without a tile: their rows are empty
-  for (int b = blockIdx.x * kPgWarps + warp; b < a.bt.B; b += gridDim.x * kPgWarps) {
+  for (int b = blockIdx.x * SL::kWarps + warp; b < a.bt.B; b += gridDim.x * SL::kWarps) {
     if (pg_tiles(a, seq_len_of(a.bt, b).len) > 0) continue;
-    const long long r0 = static_cast<long long>(b) * a.bt.T * a.Hq, n = static_cast<long long>(a.bt.T) * a.Hq;
-    for (long long i = lane; i < n * (D / 2); i += 32) pg_store2(a, r0 + i / (D / 2), D, 2 * static_cast<int>(i % (D / 2)), 0.f, 0.f);
-    for (long long i = lane; i < n; i += 32) a.lse[r0 + i] = -INFINITY;
+    const long long q0 = static_cast<long long>(b) * a.bt.T * a.Hq, n = static_cast<long long>(a.bt.T) * a.Hq;
+    for (long long i = lane; i < n * (D / 2); i += 32)
+      pg_store2(a, q0 + i / (D / 2), D, 2 * static_cast<int>(i % (D / 2)), 0.f, 0.f);
+    for (long long i = lane; i < n; i += 32) a.lse[q0 + i] = -INFINITY;
     for (int h = lane; h < a.bt.Hkv; h += 32) a.cut[static_cast<long long>(b) * a.bt.Hkv + h] = make_int2(-1, -1);
   }
 
-  // this team's run [f0, f1) of the line
-  const long long total = pg_total(a, lane);
-  const long long U = static_cast<long long>(gridDim.x) * teams;
-  const long long u = static_cast<long long>(team) * gridDim.x + blockIdx.x;
-  long long run = (total + U - 1) / U;
-  if (run < a.min_tiles) run = a.min_tiles;
-  const long long f0 = u * run, f1 = min(f0 + run, total);
-  if (f0 >= f1) return;
-  PgWalk cw;
-  pg_locate(a, f0, cw, lane);
+  const int gr = lane >> 2, qd = lane & 3;  // fragment row and column pair of this lane
+  const int team = warp / a.R, rt = warp % a.R;
+  if (team >= teams) return;  // 11 warps hold 5 teams of two, 2 of four
+  const uint32_t ring = sb + team * a.R * SL::kRing;
+  const int slot0 = team * slots;
+  const uint32_t full = sb + SL::kFull + 8u * slot0, empty = sb + SL::kEmpty + 8u * slot0;
+  const uint32_t qfull = sb + SL::kQFull + 8u * kPgQueue * team, qempty = sb + SL::kQEmpty + 8u * kPgQueue * team;
+  const PgTile* queue = reinterpret_cast<const PgTile*>(smem + SL::kMeta) + kPgQueue * team;
+  const float* scales = reinterpret_cast<const float*>(smem + SL::kScale) + slot0 * kPgKeys;
+  const int row0 = 8 * NB * rt;  // this warp's first query row
 
-  // ------------------------------------------------ loads (the leader warp)
-  // Lane i of the leader holds the cache row and the position of the 16-key
-  // unit ubase + i of the producer's pair (32 units: 16 tiles).
-  PgWalk pw = cw;
-  long long pf = f0;
-  int issued = 0, pslot = 0, ubase = 0, ent_row = 0, ent_pos = kPgNone;
-  uint32_t pphase = 0;
-  const int ps = 1 << a.bt.page_shift;
-  auto load_entries = [&]() {
-    ubase = 2 * pw.t;
-    const long long key = 16LL * (ubase + lane);
-    const int in_page = static_cast<int>(key & (ps - 1));
-    int logical = -1;
-    if (a.selected == nullptr) {
-      if (key < pw.s.len) logical = static_cast<int>(key >> a.bt.page_shift);
-    } else {
-      const int pages = (pw.s.len + ps - 1) >> a.bt.page_shift;
-      const int idx = static_cast<int>(key >> a.bt.page_shift);
-      if (idx < min(a.n_sel, pages)) {
-        const int* sel = a.selected + (static_cast<long long>(pw.b) * a.bt.Hkv + pw.h) * a.n_sel;
-        logical = sel[idx];
-        const int prev = idx > 0 ? sel[idx - 1] : -1;
-        if (logical != -1 && (logical < 0 || logical >= pages || logical <= prev)) {
-          set_status(RA_ERR_DEVICE_BOUNDS);
-          logical = -1;
-        }
-      }
-    }
-    ent_row = 0;
-    ent_pos = kPgNone;
-    if (logical >= 0) {
-      const int page = page_of(a.bt, pw.b, logical);
-      if (page >= 0) {
-        ent_row = ((page * a.bt.Hkv + pw.h) << a.bt.page_shift) + in_page;
-        ent_pos = (logical << a.bt.page_shift) + in_page;
-      }
-    }
-  };
-  // Issues the next item (K, then V of each tile); false when the ring never freed up.
-  auto issue = [&]() -> bool {
-    if (pf >= f1) return true;
-    const bool is_v = issued & 1;
-    if (a.R > 1 && issued >= slots &&
-        !__all_sync(0xffffffffu, mbar_wait(empty + 8u * pslot, pphase ^ 1u, abort_flag)))
-      return false;
-    const int l0 = 2 * pw.t - ubase;
-    const int r0 = __shfl_sync(0xffffffffu, ent_row, l0), r1 = __shfl_sync(0xffffffffu, ent_row, l0 + 1);
-    const int p0 = __shfl_sync(0xffffffffu, ent_pos, l0), p1 = __shfl_sync(0xffffffffu, ent_pos, l0 + 1);
-    if (lane == 0) {
-      const uint32_t bar = full + 8u * pslot, dst = ring + pslot * SL::kItem;
-      const CUtensorMap* tm = is_v ? &tmV : &tmK;
-      meta[pslot] = make_int2(p0, p1);
-      fence_proxy_async_smem();  // the ring slot's earlier reads precede the copy into it
-      mbar_expect_tx(bar, SL::kItem + (ET == kCacheBf16 ? 0 : kPgKeys * 4));
+  // ---- copies: items K, V, K, V ... of the queued tiles into the ring's slots.
+  // A warp instruction copies 512 bytes: copy n holds the keys from 512 / ROW * n,
+  // lane i their 16 bytes from 16 i.  The permutation of a key's chunks depends on
+  // n through kFlips values, so that many addresses serve all copies; the team's
+  // warps take the copies in turn.
+  constexpr int kCopies = SL::kItem / 512;
+  constexpr int kFlips = ROW == 256 ? 4 : ROW == 128 ? 2 : 1;
+  const uint32_t lane_off = pg_off<ROW>(lane / (ROW / 16), lane % (ROW / 16));
+  const uint8_t* const src_k = static_cast<const uint8_t*>(a.k_pages) + 16 * lane;
+  const uint8_t* const src_v = static_cast<const uint8_t*>(a.v_pages) + 16 * lane;
+  int lslot = 0, lq = 0, lr0 = 0, lr1 = 0;  // next slot and queue entry, rows of the tile being loaded
+  uint32_t lphase = 0, lqphase = 0;
+  bool lstop = false, wrapped = false, ok = true;
+  auto copy_item = [&](const uint8_t* src, const float* sc) {
+    if (a.R > 1 && wrapped) ok &= mbar_wait(empty + 8u * lslot, lphase ^ 1u, abort_flag);  // (one warp: it has read the slot)
+    const uint8_t* g0 = src + static_cast<long long>(lr0) * ROW;
+    const uint8_t* g1 = src + static_cast<long long>(lr1) * ROW - SL::kItem / 2;
+    const uint32_t dst = ring + lslot * SL::kItem;
+    if (a.R == 1) {
+      uint32_t d[kFlips];
 #pragma unroll
-      for (int half = 0; half < SL::kItem / (kPgKeys * SL::kRowBytes); ++half) {
-        const uint32_t d = dst + half * kPgKeys * SL::kRowBytes;
-        tma_load_2d(d, tm, half * 64, r0, bar);
-        if (ps == 16) tma_load_2d(d + 16 * SL::kRowBytes, tm, half * 64, r1, bar);
-      }
-      if constexpr (ET != kCacheBf16) {
-        const float* sc = is_v ? a.v_scales : a.k_scales;
-        const uint32_t sd = sb + SL::kScale + (slot0 + pslot) * kPgKeys * 4;
-        if (ps == 16) {
-          bulk_load(sd, sc + r0, 64, bar);
-          bulk_load(sd + 64, sc + r1, 64, bar);
-        } else {
-          bulk_load(sd, sc + r0, 128, bar);
-        }
-      }
+      for (int i = 0; i < kFlips; ++i) d[i] = dst + (lane_off ^ (static_cast<uint32_t>(512 / ROW * i & 7) << 4));
+#pragma unroll
+      for (int n = 0; n < kCopies; ++n) copy16(d[n % kFlips] + 512 * n, (n < kCopies / 2 ? g0 : g1) + 512 * n);
+    } else {
+      for (int n = rt; n < kCopies; n += a.R)
+        copy16(dst + 512 * n + (lane_off ^ (static_cast<uint32_t>(512 / ROW * (n % kFlips) & 7) << 4)),
+               (n < kCopies / 2 ? g0 : g1) + 512 * n);
     }
-    __syncwarp();
-    ++issued;
-    if (++pslot == slots) {
-      pslot = 0;
-      pphase ^= 1u;
+    if constexpr (ET != kCacheBf16)
+      if (rt == 0 && lane < 8)
+        copy16(sb + SL::kScale + (slot0 + lslot) * kPgKeys * 4 + 16 * lane, sc + (lane < 4 ? lr0 : lr1 - 16) + 4 * lane);
+    copies_arrive(full + 8u * lslot);
+    if (++lslot == slots) {
+      lslot = 0;
+      lphase ^= 1u;
+      wrapped = true;
     }
-    if (is_v) {
-      const int b = pw.b, h = pw.h;
-      ++pf;
-      if (pf < f1) {
-        pg_next(a, pw, lane);
-        if (pw.b != b || pw.h != h || 2 * pw.t >= ubase + 32) load_entries();
-      }
-    }
-    return true;
   };
-
-  bool ok = true;
-  if (leader) {
-    load_entries();
-    for (int i = 0; i < slots; ++i) issue();  // the first round waits for nothing
+  auto load_k = [&]() {  // the next queued tile's keys, if there is a tile
+    if (lstop) return;
+    ok &= mbar_wait(qfull + 8u * lq, lqphase, abort_flag);
+    const int4 rows = *reinterpret_cast<const int4*>(&queue[lq]);
+    lstop = !__all_sync(0xffffffffu, ok) || (queue[lq].fresh_flags & kPgStop);
+    if (lstop) return;
+    lr0 = rows.x;
+    lr1 = rows.y;
+    if (++lq == kPgQueue) {
+      lq = 0;
+      lqphase ^= 1u;
+    }
+    copy_item(src_k, a.k_scales);
+  };
+  auto load_v = [&]() {  // and its values
+    if (!lstop) copy_item(src_v, a.v_scales);
+  };
+  int slot = 0, cq = 0;
+  uint32_t phase = 0;
+  auto release = [&]() {  // this warp has read the slot
+    __syncwarp();
+    if (a.R > 1 && lane == 0) mbar_arrive(empty + 8u * slot);
+    if (++slot == slots) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  };
+  const bool odd = slots & 1;  // then a released K slot takes a V, and the other way round
+  load_k();
+  for (int i = 1; i < slots; ++i) {
+    if (i & 1) load_v();
+    else load_k();
   }
 
-  // --------------------------------------------------------------- the walk
-  int consumed = 0, cslot = 0;
-  uint32_t cphase = 0;
-  uint32_t qa[KS][4];
-  float o[NT][4], m[2], l[2];
-  int lim[2], tok[2], minlim = 0;
-  auto release = [&]() {  // this warp has read the slot; the next load into it may go out
-    __syncwarp();
-    if (a.R > 1 && lane == 0) mbar_arrive(empty + 8u * cslot);
-    ++consumed;
-    if (++cslot == slots) {
-      cslot = 0;
-      cphase ^= 1u;
-    }
-    if (leader && ok) ok = issue();
-  };
-  bool fresh_pair = true;
-  for (long long f = f0; f < f1; ++f) {
-    if (fresh_pair) {  // the query rows of this (sequence, KV head)
-      fresh_pair = false;
+  uint32_t qb[KS][NB][2];
+  float o[KS][NB][4], E[NR], l[NR], qscale = a.scale_log2;
+  int lim[NR], minlim = 0;
+  // lane parts of the shared-memory addresses; a chunk index goes in by exclusive or
+  // (the slots begin at multiples of the 256 bytes that it can change)
+  const uint32_t k_lane = ET == kCacheBf16 ? pg_off<ROW>(lane & 15, lane >> 4) : pg_off<ROW>(gr, qd);
+  const uint32_t v_lane = ET == kCacheBf16 ? pg_off<ROW>((lane & 7) + 8 * (lane >> 4), (lane >> 3) & 1)
+                                           : pg_off<ROW>(lane & 15, 0);
+  while (true) {
+    if (!__all_sync(0xffffffffu, ok)) break;
+    if (lstop && cq == lq) break;  // every loaded tile is done
+    const int4 t0 = reinterpret_cast<const int4*>(&queue[cq])[0], t1 = reinterpret_cast<const int4*>(&queue[cq])[1];
+    const PgTile tile = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+    const int fresh = tile.fresh_flags >> 8, flags = tile.fresh_flags & 255;
+    if (flags & kPgFirst) {  // the query rows of this (sequence, KV head)
       minlim = 0x7fffffff;
 #pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        const int r = 16 * rt + gr + 8 * hr;
-        const int t = r / a.groups;
-        tok[hr] = r < a.rows ? t : -1;
-        const bool real = r < a.rows && t < cw.s.fresh;
-        lim[hr] = real ? (a.causal ? cw.s.len - cw.s.fresh + t + 1 : cw.s.len) : 0;
-        if (real) minlim = min(minlim, lim[hr]);
-        m[hr] = -INFINITY;
-        l[hr] = 0.f;
-        const __nv_bfloat16* qr = a.q;
-        if (r < a.rows)
-          qr += ((static_cast<long long>(cw.b) * a.bt.T + t) * a.Hq + cw.h * a.groups + r % a.groups) * D;
-        if constexpr (ET == kCacheBf16) {
+      for (int i = 0; i < NR; ++i) {
+        const int r = row0 + 8 * (i >> 1) + 2 * qd + (i & 1), tk = r / a.groups;
+        const bool real = r < a.rows && tk < fresh;
+        lim[i] = real ? (a.causal ? tile.len - fresh + tk + 1 : tile.len) : 0;
+        if (real) minlim = min(minlim, lim[i]);
+        E[i] = -INFINITY;
+        l[i] = 0.f;
+      }
+      float qmax = 0.f;
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            qa[ks][hr] = r < a.rows ? *reinterpret_cast<const uint32_t*>(qr + 16 * ks + 2 * qd) : 0u;
-            qa[ks][2 + hr] = r < a.rows ? *reinterpret_cast<const uint32_t*>(qr + 16 * ks + 8 + 2 * qd) : 0u;
-          }
-        } else {
-          // k index of the product: step ks = 4 half + i takes columns 16 (qd + 4 half) + 4 i + {0, 2 | 1, 3}
+      for (int nb = 0; nb < NB; ++nb) {
+        const int r = row0 + 8 * nb + gr, tk = r / a.groups;
+        const bool real = r < a.rows && tk < fresh;
+        const __nv_bfloat16* qr =
+            a.q + (real ? ((static_cast<long long>(tile.b) * a.bt.T + tk) * a.Hq + tile.h * a.groups + r % a.groups) * D : 0);
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            const uint2 w = r < a.rows ? *reinterpret_cast<const uint2*>(qr + 16 * (qd + 4 * (ks >> 2)) + 4 * (ks & 3))
-                                       : make_uint2(0u, 0u);
-            qa[ks][hr] = __byte_perm(w.x, w.y, 0x5410);
-            qa[ks][2 + hr] = __byte_perm(w.x, w.y, 0x7632);
+        for (int ks = 0; ks < KS; ++ks) {
+          if constexpr (ET == kCacheBf16) {
+            qb[ks][nb][0] = real ? *reinterpret_cast<const uint32_t*>(qr + 16 * ks + 2 * qd) : 0u;
+            qb[ks][nb][1] = real ? *reinterpret_cast<const uint32_t*>(qr + 16 * ks + 8 + 2 * qd) : 0u;
+          } else {
+            // step ks = 4 half + i of the product takes columns 16 (qd + 4 half) + 4 i + {0 .. 3}
+            const uint2 x = real ? *reinterpret_cast<const uint2*>(qr + 16 * (qd + 4 * (ks >> 2)) + 4 * (ks & 3))
+                                 : make_uint2(0u, 0u);
+            qb[ks][nb][0] = x.x;
+            qb[ks][nb][1] = x.y;
+            qmax = fmaxf(qmax, fmaxf(fmaxf(fabsf(__uint_as_float(x.x << 16)), fabsf(__uint_as_float(x.x & 0xffff0000u))),
+                                     fmaxf(fabsf(__uint_as_float(x.y << 16)), fabsf(__uint_as_float(x.y & 0xffff0000u)))));
           }
         }
       }
 #pragma unroll
-      for (int x = 16; x; x >>= 1) minlim = min(minlim, __shfl_xor_sync(0xffffffffu, minlim, x));
+      for (int x = 16; x; x >>= 1) {
+        minlim = min(minlim, __shfl_xor_sync(0xffffffffu, minlim, x));
+        if (ET != kCacheBf16) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, x));
+      }
+      if constexpr (ET != kCacheBf16) {
+        // 2^up brings the largest query to [2^14, 2^15), within what an fp32 factor can say
+        const int up = min(max(127 + 14 - static_cast<int>(__float_as_uint(qmax) >> 23), -110), 110);
+        const float mul = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+        qscale = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const uint32_t x = qb[ks][nb][0], y = qb[ks][nb][1];
+            const uint32_t xf = pack_f16x2(__uint_as_float(x << 16) * mul, __uint_as_float(x & 0xffff0000u) * mul);
+            const uint32_t yf = pack_f16x2(__uint_as_float(y << 16) * mul, __uint_as_float(y & 0xffff0000u) * mul);
+            // int8 codes pair up as bytes 0, 2 and 1, 3; e4m3 ones as 0, 1 and 2, 3
+            qb[ks][nb][0] = ET == kCacheI8 ? __byte_perm(xf, yf, 0x5410) : xf;
+            qb[ks][nb][1] = ET == kCacheI8 ? __byte_perm(xf, yf, 0x7632) : yf;
+          }
+      }
+#pragma unroll
+      for (int c = 0; c < KS; ++c)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) o[c][nb][0] = o[c][nb][1] = o[c][nb][2] = o[c][nb][3] = 0.f;
     }
 
-    // ---- scores of the tile's 32 keys
-    ok = ok && __all_sync(0xffffffffu, mbar_wait(full + 8u * cslot, cphase, abort_flag));
-    if (!ok) break;
-    const uint32_t kt = ring + cslot * SL::kItem;
-    const int2 pos = meta[cslot];
-    float s[4][4];
+    // ---- scores: s[mb][nb] holds keys 16 mb + gr, + 8 and rows 8 nb + 2 qd, + 1
+    ok &= mbar_wait(full + 8u * slot, phase, abort_flag);
+    const uint32_t kt = ring + slot * SL::kItem + k_lane;
+    float s[2][NB][4];
+    float xc[4];  // factors of the scores of keys gr + 8 i
 #pragma unroll
-    for (int nb = 0; nb < 4; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+    for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) s[mb][nb][0] = s[mb][nb][1] = s[mb][nb][2] = s[mb][nb][3] = 0.f;
     if constexpr (ET == kCacheBf16) {
 #pragma unroll
-      for (int kp = 0; kp < KS / 2; ++kp)
+      for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb) {
-          uint32_t kb[4];
-          ldsm_x4(kt + pg_off<D, ET>(8 * nb + (lane & 7), 4 * kp + (lane >> 3)), kb);
-          mma_16816(s[nb], qa[2 * kp], kb[0], kb[1]);
-          mma_16816(s[nb], qa[2 * kp + 1], kb[2], kb[3]);
+        for (int mb = 0; mb < 2; ++mb) {
+          uint32_t ka[4];
+          ldsm_x4((kt ^ (32u * ks)) + 16 * ROW * mb, ka);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) pg_mma<ET>(s[mb][nb], ka, qb[ks][nb][0], qb[ks][nb][1]);
         }
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nb][e] *= a.scale_log2;
+      for (int i = 0; i < 4; ++i) xc[i] = a.scale_log2;
     } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xc[i] = scales[slot * kPgKeys + gr + 8 * i] * qscale;
 #pragma unroll
       for (int half = 0; half < KS / 4; ++half)
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb) {
-          uint4 w4;
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(w4.x), "=r"(w4.y), "=r"(w4.z), "=r"(w4.w)
-                       : "r"(kt + pg_off<D, ET>(8 * nb + gr, qd + 4 * half)));
-          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+        for (int mb = 0; mb < 2; ++mb) {
+          uint32_t c[2][4];  // keys gr and gr + 8 of the 16
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_16816(s[nb], qa[4 * half + i], codes_to_bf16<ET>(w[i]), codes_to_bf16<ET>(w[i] >> 8));
+          for (int i = 0; i < 2; ++i)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(c[i][0]), "=r"(c[i][1]), "=r"(c[i][2]), "=r"(c[i][3])
+                         : "r"((kt ^ (64u * half)) + (16 * mb + 8 * i) * ROW));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t ka[4];
+            if constexpr (ET == kCacheI8) {
+              ka[0] = i8_to_f16(c[0][i]);
+              ka[1] = i8_to_f16(c[1][i]);
+              ka[2] = i8_to_f16(c[0][i] >> 8);
+              ka[3] = i8_to_f16(c[1][i] >> 8);
+            } else {
+              ka[0] = e4m3_to_f16<0>(c[0][i]);
+              ka[1] = e4m3_to_f16<0>(c[1][i]);
+              ka[2] = e4m3_to_f16<1>(c[0][i]);
+              ka[3] = e4m3_to_f16<1>(c[1][i]);
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) pg_mma<ET>(s[mb][nb], ka, qb[4 * half + i][nb][0], qb[4 * half + i][nb][1]);
+          }
         }
-      const float* ksc = reinterpret_cast<const float*>(smem + SL::kScale) + (slot0 + cslot) * kPgKeys;
-#pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
-        const float2 sc = *reinterpret_cast<const float2*>(ksc + 8 * nb + 2 * qd);
-        s[nb][0] *= sc.x * a.scale_log2;
-        s[nb][1] *= sc.y * a.scale_log2;
-        s[nb][2] *= sc.x * a.scale_log2;
-        s[nb][3] *= sc.y * a.scale_log2;
-      }
     }
     release();
+    if (odd) load_v();
+    else load_k();
+    ok &= mbar_wait(full + 8u * slot, phase, abort_flag);  // V, and its scales
 
-    // ---- mask, running maximum, weights
-    const bool masked = pos.x + 16 > minlim || pos.y + 16 > minlim;  // the same for the whole warp
-    uint32_t seen = 0xffffu;  // bit 4 nb + e: this lane's score s[nb][e] is of a visible key
+    // ---- weights
+    const uint32_t vt = ring + slot * SL::kItem;
+    const bool masked = tile.p0 + 16 > minlim || tile.p1 + 16 > minlim;  // the same for the whole warp
+    uint32_t seen = 0xffffffffu;  // bit 8 mb + 4 nb + e: this lane's s[mb][nb][e] is of a visible key
     if (masked) {
       seen = 0u;
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb)
+      for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int kp = (nb < 2 ? pos.x + 8 * nb : pos.y + 8 * (nb - 2)) + 2 * qd + (e & 1);
-          if (kp < lim[e >> 1]) seen |= 1u << (4 * nb + e);
-          else s[nb][e] = -INFINITY;
-        }
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if ((mb ? tile.p1 : tile.p0) + gr + 8 * (e >> 1) < lim[2 * nb + (e & 1)]) seen |= 1u << (8 * mb + 4 * nb + e);
     }
-    float mx[2];
-#pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      float x = fmaxf(fmaxf(fmaxf(s[0][2 * hr], s[0][2 * hr + 1]), fmaxf(s[1][2 * hr], s[1][2 * hr + 1])),
-                      fmaxf(fmaxf(s[2][2 * hr], s[2][2 * hr + 1]), fmaxf(s[3][2 * hr], s[3][2 * hr + 1])));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-      mx[hr] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-    }
-    if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
-#pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        const float mn = fmaxf(m[hr], mx[hr]);
-        const float al = m[hr] == -INFINITY ? 0.f : fast_exp2(m[hr] - mn);  // mn >= m > -inf there
-        m[hr] = mn;
-        l[hr] *= al;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          o[nt][2 * hr] *= al;
-          o[nt][2 * hr + 1] *= al;
-        }
-      }
-    }
-#pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      const float base = m[hr] == -INFINITY ? 0.f : m[hr];
-#pragma unroll
-      for (int nb = 0; nb < 4; ++nb)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float p = fast_exp2(s[nb][2 * hr + e] - base);
-          s[nb][2 * hr + e] = p;
-          l[hr] += p;
-        }
-    }
-
-    // ---- o += P V
-    ok = ok && __all_sync(0xffffffffu, mbar_wait(full + 8u * cslot, cphase, abort_flag));
-    if (!ok) break;
-    const uint32_t vt = ring + cslot * SL::kItem;
+    float vs[4] = {1.f, 1.f, 1.f, 1.f};
     if constexpr (ET != kCacheBf16) {
-      const float* vsc = reinterpret_cast<const float*>(smem + SL::kScale) + (slot0 + cslot) * kPgKeys;
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
-        const float2 sc = *reinterpret_cast<const float2*>(vsc + 8 * nb + 2 * qd);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)  // a masked key's scale may be anything
-          s[nb][e] = (seen >> (4 * nb + e)) & 1u ? s[nb][e] * ((e & 1) ? sc.y : sc.x) : 0.f;
+      for (int i = 0; i < 4; ++i) {
+        vs[i] = scales[slot * kPgKeys + gr + 8 * i];
+        if (vs[i] == 0.f) vs[i] = 1.f;  // a row of zeros: its codes are 0, its weight still counts in l
       }
     }
+    float w[2][NB][4], lt[NR], top;
+    auto weigh = [&](auto with_mask) {  // w_j and their sums against E as it is
+      constexpr bool kMask = decltype(with_mask)::value;
+      top = 0.f;
+#pragma unroll
+      for (int i = 0; i < NR; ++i) lt[i] = 0.f;
+#pragma unroll
+      for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool hide = kMask && !((seen >> (8 * mb + 4 * nb + e)) & 1u);
+            float p = fast_exp2(fmaf(s[mb][nb][e], xc[2 * mb + (e >> 1)], -E[2 * nb + (e & 1)]));
+            if (hide) p = 0.f;
+            lt[2 * nb + (e & 1)] += p;
+            if constexpr (ET != kCacheBf16) p *= vs[2 * mb + (e >> 1)];
+            if (hide) p = 0.f;  // an unseen key's scale may be anything
+            w[mb][nb][e] = p;
+          }
+          top = fmax3(fmax3(top, w[mb][nb][0], w[mb][nb][1]), w[mb][nb][2], w[mb][nb][3]);
+        }
+    };
+    if (masked) weigh(std::true_type{});
+    else weigh(std::false_type{});
+    if (__any_sync(0xffffffffu, top > kPgLazy)) {  // the first tile of a pair always comes here (E = -inf)
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        float y = -INFINITY;  // largest x_j + log2 vs_j of the row's visible keys
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+          for (int k8 = 0; k8 < 2; ++k8) {
+            const int e = 2 * k8 + (i & 1);
+            float x = s[mb][i >> 1][e] * xc[2 * mb + k8];
+            if constexpr (ET != kCacheBf16) x += __log2f(vs[2 * mb + k8]);
+            if ((seen >> (8 * mb + 4 * (i >> 1) + e)) & 1u) y = fmaxf(y, x);
+          }
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, x));
+        const float En = fmaxf(E[i], y);
+        const float al = E[i] == -INFINITY ? 0.f : fast_exp2(E[i] - En);
+        E[i] = En;
+        l[i] *= al;
+#pragma unroll
+        for (int c = 0; c < KS; ++c) {
+          o[c][i >> 1][i & 1] *= al;
+          o[c][i >> 1][2 + (i & 1)] *= al;
+        }
+      }
+      weigh(std::true_type{});
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i) l[i] += lt[i];
+
+    // ---- o += V^T W
     bool slow = false;
     if (ET == kCacheBf16 && masked) {
-      // A row that no query row sees may hold anything (old tokens, memory never
+      // A key that a row does not see may hold anything (old tokens, memory never
       // written): 0 * NaN must not reach the sum.  Codes of 8 bits are finite.
       uint32_t big = 0;
 #pragma unroll
-      for (int i = 0; i < NT; i += 2)
+      for (int c = 0; c < KS; ++c)
 #pragma unroll
         for (int kh = 0; kh < 2; ++kh) {
           uint32_t r4[4];
-          ldsm_x4_t(vt + pg_off<D, ET>(16 * kh + (lane & 15), i + (lane >> 4)), r4);
+          ldsm_x4(vt + pg_off<ROW>(16 * kh + (lane & 15), 2 * c + (lane >> 4)), r4);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             big |= (r4[j] & 0x7f80u) == 0x7f80u;
@@ -556,143 +798,139 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     if (!slow) {
 #pragma unroll
       for (int kh = 0; kh < 2; ++kh) {
-        // the weights as bf16 terms: rounded, the remainder rounded, and once more for an fp32 output
-        uint32_t pa[3][4];
+        uint32_t pb[3][NB][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x = s[2 * kh + (i >> 1)][2 * (i & 1)], y = s[2 * kh + (i >> 1)][2 * (i & 1) + 1];
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int term = 0; term < 3; ++term) {
-            pa[term][i] = pack_bf16x2(x, y);
-            x -= __uint_as_float(pa[term][i] << 16);
-            y -= __uint_as_float(pa[term][i] & 0xffff0000u);
+          for (int k8 = 0; k8 < 2; ++k8) {
+            uint32_t t[3];
+            split_pair<ET>(w[kh][nb][2 * k8], w[kh][nb][2 * k8 + 1], !a.out_bf16, t);
+            pb[0][nb][k8] = transpose_8x8(t[0]);
+            pb[1][nb][k8] = transpose_8x8(t[1]);
+            pb[2][nb][k8] = ET == kCacheBf16 && !a.out_bf16 ? transpose_8x8(t[2]) : 0u;
           }
-        }
 #pragma unroll
-        for (int c = 0; c < NT / 2; ++c) {  // 16 output columns
-          uint32_t b[2][2];
+        for (int c = 0; c < KS; ++c) {  // 16 output columns
+          uint32_t va[4];
           if constexpr (ET == kCacheBf16) {
-            uint32_t r4[4];
-            ldsm_x4_t(vt + pg_off<D, ET>(16 * kh + (lane & 15), 2 * c + (lane >> 4)), r4);
-            b[0][0] = r4[0];
-            b[0][1] = r4[1];
-            b[1][0] = r4[2];
-            b[1][1] = r4[3];
+            ldsm_x4_t(((vt + v_lane) ^ (32u * c)) + 16 * ROW * kh, va);
           } else {
-            // 16-bit units of a transposed 8x8 load are two neighbouring codes of
-            // a key: the even columns of the 16 make one n8 block, the odd ones another
+            // 16-bit units of a transposed 8x8 load are two neighbouring codes of a
+            // key: the even columns of the 16 make rows 0 - 7, the odd ones rows 8 - 15
             uint32_t r2[2];
             asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
                          : "=r"(r2[0]), "=r"(r2[1])
-                         : "r"(vt + pg_off<D, ET>(16 * kh + (lane & 15), c)));
-            b[0][0] = codes_to_bf16<ET>(r2[0]);
-            b[0][1] = codes_to_bf16<ET>(r2[1]);
-            b[1][0] = codes_to_bf16<ET>(r2[0] >> 8);
-            b[1][1] = codes_to_bf16<ET>(r2[1] >> 8);
+                         : "r"(((vt + v_lane) ^ (16u * c)) + 16 * ROW * kh));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if constexpr (ET == kCacheI8) {
+                va[2 * j] = i8_to_f16(r2[j]);
+                va[2 * j + 1] = i8_to_f16(r2[j] >> 8);
+              } else {
+                const uint32_t eo = __byte_perm(r2[j], 0u, 0x3120);  // bytes 0, 2, 1, 3
+                va[2 * j] = e4m3_to_f16<0>(eo);
+                va[2 * j + 1] = e4m3_to_f16<1>(eo);
+              }
+            }
           }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            mma_16816(o[2 * c + e], pa[0], b[e][0], b[e][1]);
-            mma_16816(o[2 * c + e], pa[1], b[e][0], b[e][1]);
-            if (!a.out_bf16) mma_16816(o[2 * c + e], pa[2], b[e][0], b[e][1]);
-          }
+          for (int term = 0; term < 2; ++term)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) pg_mma<ET>(o[c][nb], va, pb[term][nb][0], pb[term][nb][1]);
+          if (ET == kCacheBf16 && !a.out_bf16)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) pg_mma<ET>(o[c][nb], va, pb[2][nb][0], pb[2][nb][1]);
         }
       }
     } else {
       // key by key, each row taking only the keys that it sees
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb)
+      for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          for (int x = 0; x < 4; ++x) {
-            const int src = (lane & ~3) | x, j = 8 * nb + 2 * x + e;
-            const float p0 = __shfl_sync(0xffffffffu, s[nb][e], src), p1 = __shfl_sync(0xffffffffu, s[nb][2 + e], src);
+        for (int k8 = 0; k8 < 2; ++k8)
+          for (int x = 0; x < 8; ++x) {
+            const int src = 4 * x + qd, j = 16 * mb + 8 * k8 + x;
             const uint32_t sn = __shfl_sync(0xffffffffu, seen, src);
-            const bool see0 = (sn >> (4 * nb + e)) & 1u, see1 = (sn >> (4 * nb + 2 + e)) & 1u;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              uint32_t w;
-              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(vt + pg_off<D, ET>(j, nt) + 4 * qd));
-              const float v0 = __uint_as_float(w << 16), v1 = __uint_as_float(w & 0xffff0000u);
-              if (see0) {
-                o[nt][0] = fmaf(p0, v0, o[nt][0]);
-                o[nt][1] = fmaf(p0, v1, o[nt][1]);
-              }
-              if (see1) {
-                o[nt][2] = fmaf(p1, v0, o[nt][2]);
-                o[nt][3] = fmaf(p1, v1, o[nt][3]);
-              }
+            for (int i = 0; i < NR; ++i) {
+              const int e = 2 * k8 + (i & 1);
+              const float p = __shfl_sync(0xffffffffu, w[mb][i >> 1][e], src);
+              if (!((sn >> (8 * mb + 4 * (i >> 1) + e)) & 1u)) continue;
+#pragma unroll
+              for (int c = 0; c < KS; ++c)
+#pragma unroll
+                for (int d8 = 0; d8 < 2; ++d8) {
+                  uint16_t v;
+                  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(vt + pg_off<ROW>(j, 2 * c + d8) + 2 * gr));
+                  o[c][i >> 1][2 * d8 + (i & 1)] = fmaf(p, __uint_as_float(static_cast<uint32_t>(v) << 16), o[c][i >> 1][2 * d8 + (i & 1)]);
+                }
             }
           }
     }
     release();
+    if (odd) load_k();
+    else load_v();
+    if (lane == 0) mbar_arrive(qempty + 8u * cq);  // (tile is in registers)
+    if (++cq == kPgQueue) cq = 0;
 
     // ---- the end of the pair, or of this team's part of it
-    if (cw.t + 1 == cw.nt || f + 1 == f1) {
-      const long long seg0 = f - cw.t;  // the pair's first tile
-      const bool owner = seg0 >= f0, whole = owner && cw.t + 1 == cw.nt;
-      if (leader && lane == 0 && owner)
-        a.cut[static_cast<long long>(cw.b) * a.bt.Hkv + cw.h] =
-            whole ? make_int2(-1, -1) : make_int2(static_cast<int>(u), static_cast<int>((seg0 + cw.nt - 1) / run));
+    if (flags & kPgLast) {
+      const long long u = static_cast<long long>(team) * gridDim.x + blockIdx.x;
 #pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        l[hr] += __shfl_xor_sync(0xffffffffu, l[hr], 1);
-        l[hr] += __shfl_xor_sync(0xffffffffu, l[hr], 2);
-        if (tok[hr] < 0) continue;
-        const int r = 16 * rt + gr + 8 * hr;
-        const bool has = lim[hr] > 0 && !(l[hr] == 0.f);  // a NaN sum stays
-        if (whole) {
-          const long long row = (static_cast<long long>(cw.b) * a.bt.T + tok[hr]) * a.Hq + cw.h * a.groups + r % a.groups;
-          const float inv = has ? 1.f / l[hr] : 0.f;
+      for (int i = 0; i < NR; ++i) {
 #pragma unroll
-          for (int c = 0; c < NT / 2; ++c) {
-            const float x0 = has ? o[2 * c][2 * hr] * inv : 0.f, x1 = has ? o[2 * c][2 * hr + 1] * inv : 0.f;
-            const float y0 = has ? o[2 * c + 1][2 * hr] * inv : 0.f, y1 = has ? o[2 * c + 1][2 * hr + 1] * inv : 0.f;
+        for (int x = 4; x < 32; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+        const int r = row0 + 8 * (i >> 1) + 2 * qd + (i & 1);
+        if (r >= a.rows) continue;
+        const bool has = lim[i] > 0 && !(l[i] == 0.f);  // a NaN sum stays
+        const int nb = i >> 1, e = i & 1;
+        if (flags & kPgWhole) {
+          const long long row =
+              (static_cast<long long>(tile.b) * a.bt.T + r / a.groups) * a.Hq + tile.h * a.groups + r % a.groups;
+          const float inv = has ? 1.f / l[i] : 0.f;
+#pragma unroll
+          for (int c = 0; c < KS; ++c) {
+            const float x = has ? o[c][nb][e] * inv : 0.f, y = has ? o[c][nb][2 + e] * inv : 0.f;
             if constexpr (ET == kCacheBf16) {
-              pg_store2(a, row, D, 16 * c + 2 * qd, x0, x1);
-              pg_store2(a, row, D, 16 * c + 8 + 2 * qd, y0, y1);
+              pg_store1(a, row, D, 16 * c + gr, x);
+              pg_store1(a, row, D, 16 * c + 8 + gr, y);
             } else {
-              pg_store2(a, row, D, 16 * c + 4 * qd, x0, y0);
-              pg_store2(a, row, D, 16 * c + 4 * qd + 2, x1, y1);
+              pg_store2(a, row, D, 16 * c + 2 * gr, x, y);
             }
           }
-          if (qd == 0) a.lse[row] = has ? (m[hr] + log2f(l[hr])) * 0.6931471805599453f : -INFINITY;
+          if (gr == 0) a.lse[row] = has ? (E[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
         } else {
-          const long long pr = (2 * u + (owner ? 1 : 0)) * a.rows + r;
+          const long long pr = (2 * u + (flags & kPgOwner ? 1 : 0)) * a.rows + r;
           float* dst = a.part_o + pr * D;
 #pragma unroll
-          for (int c = 0; c < NT / 2; ++c) {
-            const float x0 = o[2 * c][2 * hr], x1 = o[2 * c][2 * hr + 1];
-            const float y0 = o[2 * c + 1][2 * hr], y1 = o[2 * c + 1][2 * hr + 1];
+          for (int c = 0; c < KS; ++c) {
             if constexpr (ET == kCacheBf16) {
-              *reinterpret_cast<float2*>(dst + 16 * c + 2 * qd) = make_float2(x0, x1);
-              *reinterpret_cast<float2*>(dst + 16 * c + 8 + 2 * qd) = make_float2(y0, y1);
+              dst[16 * c + gr] = o[c][nb][e];
+              dst[16 * c + 8 + gr] = o[c][nb][2 + e];
             } else {
-              *reinterpret_cast<float4*>(dst + 16 * c + 4 * qd) = make_float4(x0, y0, x1, y1);
+              *reinterpret_cast<float2*>(dst + 16 * c + 2 * gr) = make_float2(o[c][nb][e], o[c][nb][2 + e]);
             }
           }
-          if (qd == 0) a.part_ml[pr] = has ? make_float2(m[hr], l[hr]) : make_float2(-INFINITY, 0.f);
+          if (gr == 0) a.part_ml[pr] = has ? make_float2(E[i], l[i]) : make_float2(-INFINITY, 0.f);
         }
       }
-      fresh_pair = true;
     }
-    if (f + 1 < f1) pg_next(a, cw, lane);
   }
-  if (!ok && leader && lane == 0)  // let every copy already issued land before shared memory is released
-    for (int i = consumed; i < issued; ++i) mbar_drain(full + 8u * (i % slots), (i / slots) & 1);
+  copies_wait_all();  // none is left in the normal course
 }
 
-// Joins the parts of the cut pairs: with M = max m_i over the parts,
-// l = sum 2^(m_i - M) l_i, out = sum 2^(m_i - M) o_i / l.  WPR warps share a
-// row (8 where rows are few and parts many, 1 otherwise); the lanes hold its D
-// columns.  Every part is read once, in team order: the result does not depend
-// on scheduling.
-template <int D, int WPR>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedArgs a, int max_teams) {
-  constexpr int kPer = D / 32, kBatch = 4;
-  __shared__ float s_acc[WPR == 1 ? 1 : 8][D];
+// Joins the parts of the cut pairs: with M = max E_i over the parts,
+// l = sum 2^(E_i - M) l_i, out = sum 2^(E_i - M) o_i / l.  WPR warps of a CTA of
+// NW share a row; the lanes hold its D columns.  32 to a row where rows are few
+// and their parts many (592 for one token against 1M keys), one where the rows
+// alone fill the GPU.  Every part is read once and in a fixed order: the result
+// does not depend on scheduling.
+template <int D, int WPR, int NW>
+__global__ void __launch_bounds__(32 * NW) paged_combine_kernel(const __grid_constant__ PagedArgs a, int max_teams) {
+  constexpr int kPer = D / 32, kBatch = NW == 32 ? 4 : 8;
+  __shared__ float s_acc[WPR == 1 ? 1 : NW][D], s_l[NW], s_m[NW];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long id = static_cast<long long>(blockIdx.x) * (8 / WPR) + warp / WPR;
+  const long long id = static_cast<long long>(blockIdx.x) * (NW / WPR) + warp / WPR;
   const int w0 = warp % WPR;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long pairs = static_cast<long long>(a.bt.B) * a.bt.Hkv;
@@ -702,40 +940,39 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   const int2 cut = a.cut[pair];
   if (cut.x < 0 || cut.y <= cut.x || cut.y >= max_teams) return;  // the last: records of a call that timed out
   auto part = [&](int t) { return (2LL * t + (t == cut.x ? 1 : 0)) * a.rows + r; };
-  float M = -INFINITY;
-  for (int t = cut.x + lane; t <= cut.y; t += 32) M = fmaxf(M, a.part_ml[part(t)].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float base = M == -INFINITY ? 0.f : M;
-  float L = 0.f;
-  for (int t = cut.x + lane; t <= cut.y; t += 32) {
-    const float2 ml = a.part_ml[part(t)];
-    L += fast_exp2(ml.x - base) * ml.y;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  float acc[kPer];
+  // this warp's parts w0, w0 + WPR, ... against their own maximum
+  float M = -INFINITY, L = 0.f, acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
   for (int t0 = cut.x + w0; t0 <= cut.y; t0 += WPR * kBatch) {
-    float v[kBatch][kPer], mm[kBatch];
+    float v[kBatch][kPer];
+    float2 ml[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int t = t0 + WPR * k;
-      mm[k] = -INFINITY;
+      ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int e = 0; e < kPer; ++e) v[k][e] = 0.f;
       if (t <= cut.y) {
-        mm[k] = a.part_ml[part(t)].x;
+        ml[k] = a.part_ml[part(t)];
         const float* src = a.part_o + part(t) * D + kPer * lane;
 #pragma unroll
         for (int e = 0; e < kPer; ++e) v[k][e] = src[e];
       }
     }
+    float mb = M;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) mb = fmaxf(mb, ml[k].x);
+    const float old = M == -INFINITY ? 0.f : fast_exp2(M - mb);
+    M = mb;
+    L *= old;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] *= old;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      if (mm[k] == -INFINITY) continue;  // a part in which the row sees no key
-      const float w = fast_exp2(mm[k] - base);
+      if (ml[k].y == 0.f) continue;  // a part in which the row sees no key
+      const float w = ml[k].x == -INFINITY ? 1.f : fast_exp2(ml[k].x - M);  // -inf with a sum: NaN scores
+      L = fmaf(w, ml[k].y, L);
 #pragma unroll
       for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
     }
@@ -743,12 +980,31 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   if constexpr (WPR > 1) {
 #pragma unroll
     for (int e = 0; e < kPer; ++e) s_acc[warp][kPer * lane + e] = acc[e];
+    if (lane == 0) {
+      s_l[warp] = L;
+      s_m[warp] = M;
+    }
     __syncthreads();
     if (w0 != 0) return;
+    // lane w: the factor of warp w's result
+    const float mw = lane < WPR ? s_m[warp + lane] : -INFINITY;
+    M = mw;
 #pragma unroll
-    for (int w = 1; w < WPR; ++w)
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float lw = lane < WPR ? s_l[warp + lane] : 0.f;
+    const float fw = lw == 0.f ? 0.f : mw == -INFINITY ? 1.f : fast_exp2(mw - M);
+    L = fw * lw;
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] += s_acc[warp + w][kPer * lane + e];
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll 8
+    for (int w = 0; w < WPR; ++w) {
+      const float f = __shfl_sync(0xffffffffu, fw, w);
+      if (f != 0.f)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(f, s_acc[warp + w][kPer * lane + e], acc[e]);
+    }
   }
   const bool has = !(L == 0.f);
   const float inv = has ? 1.f / L : 0.f;

@@ -114,7 +114,7 @@ def test_paged_decode_refuses(ra, kw, status):
 
 
 def test_paged_decode_workspace(ra):
-    # teams of a full grid: 8 warps an SM, 1, 2 or 4 to a team; two cut pairs each
+    # teams of a full grid: 8 warps an SM at least, 1, 2 or 4 to a team; two cut pairs each
     for Tq, Hq, Hkv, per in ((1, 8, 2, 8), (4, 32, 8, 8), (5, 4, 1, 4), (1, 64, 1, 2)):
         rows = Hq // Hkv * Tq
         n = ra.ra_paged_decode_workspace(3, Tq, Hq, Hkv, 128)
