@@ -17,6 +17,7 @@ torch.distributed point-to-point messages.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -447,51 +448,56 @@ def ra_decode_attention(q, k, v, causal: bool = True, n_splits: int = 0, out=Non
 _CACHE_DTYPES = {torch.bfloat16: RA_BF16, torch.int8: RA_I8, torch.float8_e4m3fn: RA_E4M3}
 
 
-def _expect(t: torch.Tensor | None, name: str, dtype, shape, device) -> int | None:
-    """The address of t, checked: contiguous, on `device`, of this dtype and shape."""
+def _expect(t: torch.Tensor | None, name: str, dtype, shape, device: int) -> int | None:
+    """The address of t, checked: contiguous, on CUDA device `device`, of this dtype and shape."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}, "
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on cuda:{device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
 def _paged(k_pages, v_pages, k_scales, v_scales, key_bounds, page_table, seq_lens, new_lens) -> ra_paged_cache:
     """The C argument of a cache and its batch (shapes and devices checked)."""
-    dev = k_pages.device
-    if dev.type != "cuda":
+    if not k_pages.is_cuda:
         raise ValueError("tensors must be contiguous CUDA tensors")
-    if k_pages.dim() != 4 or k_pages.dtype not in _CACHE_DTYPES:
+    dev, dtype, shape, tab = k_pages.get_device(), k_pages.dtype, k_pages.shape, page_table.shape
+    if len(shape) != 4 or dtype not in _CACHE_DTYPES:
         raise ValueError("k_pages must be [n_pages, Hkv, page_size, D] in bfloat16, int8 or float8_e4m3fn")
-    if page_table.dim() != 2:
+    if len(tab) != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    n_pages, Hkv, page_size, D = k_pages.shape
-    B, max_pages = page_table.shape
-    code = _CACHE_DTYPES[k_pages.dtype]
+    n_pages, Hkv, page_size, D = shape
+    B, max_pages = tab
+    code = _CACHE_DTYPES[dtype]
     if (code == RA_BF16) != (k_scales is None) or (code == RA_BF16) != (v_scales is None):
         raise ValueError("an 8-bit cache has k_scales and v_scales, a bfloat16 one has none")
     f32, i32 = torch.float32, torch.int32
-    rows = (n_pages, Hkv, page_size)
+    rows, lens = (n_pages, Hkv, page_size), (B,)
     return ra_paged_cache(
-        _expect(k_pages, "k_pages", k_pages.dtype, k_pages.shape, dev),
-        _expect(v_pages, "v_pages", k_pages.dtype, k_pages.shape, dev),
+        _expect(k_pages, "k_pages", dtype, shape, dev), _expect(v_pages, "v_pages", dtype, shape, dev),
         _expect(k_scales, "k_scales", f32, rows, dev), _expect(v_scales, "v_scales", f32, rows, dev),
         _expect(key_bounds, "key_bounds", torch.bfloat16, (n_pages, Hkv, 2, D), dev), code, n_pages, page_size, Hkv, D,
-        _expect(page_table, "page_table", i32, page_table.shape, dev), B, max_pages,
-        _expect(seq_lens, "seq_lens", i32, (B,), dev), _expect(new_lens, "new_lens", i32, (B,), dev))
+        _expect(page_table, "page_table", i32, tab, dev), B, max_pages,
+        _expect(seq_lens, "seq_lens", i32, lens, dev), _expect(new_lens, "new_lens", i32, lens, dev))
 
 
-def _call_on(dev: torch.device, stream, fn, what: str, *args) -> None:
-    """fn(*args, stream) with `dev` current, on the given stream or on dev's
-    current one (not another device's)."""
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if torch.cuda.current_device() != dev.index:
+# the current stream's handle of a device; torch.cuda.current_stream builds a Stream object to say the same
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _call_on(dev: int, stream, fn, what: str, *args) -> None:
+    """fn(*args, stream) with CUDA device `dev` current, on the given stream or on
+    dev's current one (not another device's)."""
+    handle = _raw_stream(dev) if stream is None else _stream(stream)
+    if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)), what)
+            status = fn(*args, handle)
     else:
-        _check(fn(*args, _stream(stream)), what)
+        status = fn(*args, handle)
+    if status != RA_OK:
+        raise RAError(status, what)
 
 
 def ra_cache_append(k, v, k_pages, v_pages, page_table, seq_lens, new_lens=None, k_scales=None, v_scales=None,
@@ -504,7 +510,7 @@ def ra_cache_append(k, v, k_pages, v_pages, page_table, seq_lens, new_lens=None,
     if k.dim() != 4:
         raise ValueError("k must be [B, T, Hkv, D]")
     T = k.shape[1]
-    shape, dev = (c.B, T, c.Hkv, c.D), k_pages.device
+    shape, dev = (c.B, T, c.Hkv, c.D), k_pages.get_device()
     _call_on(dev, stream, _lib.ra_cache_append, "ra_cache_append", ctypes.byref(c),
              _expect(k, "k", k.dtype, shape, dev), _expect(v, "v", k.dtype, shape, dev), _dtype_code(k.dtype), T)
 
@@ -515,17 +521,18 @@ def ra_cache_read(k_pages, v_pages, page_table, seq_lens, T: int, first: int = 0
     [B, T, Hkv, D], zero at and behind seq_lens[b]; out_dtype bfloat16 (default)
     or float32."""
     c = _paged(k_pages, v_pages, k_scales, v_scales, None, page_table, seq_lens, None)
-    shape, dev = (c.B, T, c.Hkv, c.D), k_pages.device
+    shape, dev = (c.B, T, c.Hkv, c.D), k_pages.get_device()
     odt = out_dtype or (k.dtype if k is not None else v.dtype if v is not None else torch.bfloat16)
     if k is None:
-        k = torch.empty(shape, dtype=odt, device=dev)
+        k = k_pages.new_empty(shape, dtype=odt)
     if v is None:
-        v = torch.empty(shape, dtype=odt, device=dev)
+        v = k_pages.new_empty(shape, dtype=odt)
     _call_on(dev, stream, _lib.ra_cache_read, "ra_cache_read", ctypes.byref(c), first, T,
              _expect(k, "k", odt, shape, dev), _expect(v, "v", odt, shape, dev), _dtype_code(odt))
     return k, v
 
 
+@functools.lru_cache(maxsize=None)
 def ra_paged_decode_workspace(B, Tq, Hq, Hkv, D) -> int:
     n = _lib.ra_paged_decode_workspace(B, Tq, Hq, Hkv, D)
     if n == ctypes.c_size_t(-1).value:
@@ -545,19 +552,19 @@ def ra_paged_decode_attention(q, k_pages, v_pages, page_table, seq_lens, new_len
     if q.dim() != 4:
         raise ValueError("q must be [B, Tq, Hq, D]")
     _, Tq, Hq, _ = q.shape
-    shape, dev = (c.B, Tq, Hq, c.D), k_pages.device
+    shape, dev = (c.B, Tq, Hq, c.D), k_pages.get_device()
     odt = out_dtype or (out.dtype if out is not None else torch.float32)
     if out is None:
-        out = torch.empty(shape, dtype=odt, device=dev)
+        out = q.new_empty(shape, dtype=odt)
     if lse is None:
-        lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
+        lse = q.new_empty(shape[:3], dtype=torch.float32)
     n_sel = 0
     if selected is not None:
         if selected.dim() != 3:
             raise ValueError("selected must be [B, Hkv, n_sel]")
         n_sel = selected.shape[2]
     if workspace is None:
-        workspace = torch.empty(ra_paged_decode_workspace(c.B, Tq, Hq, c.Hkv, c.D), dtype=torch.uint8, device=dev)
+        workspace = k_pages.new_empty(ra_paged_decode_workspace(c.B, Tq, Hq, c.Hkv, c.D), dtype=torch.uint8)
     _call_on(dev, stream, _lib.ra_paged_decode_attention, "ra_paged_decode_attention", _expect(q, "q", q.dtype, shape, dev),
              _dtype_code(q.dtype), ctypes.byref(c), Tq, Hq, int(bool(causal)),
              _expect(selected, "selected", torch.int32, (c.B, c.Hkv, n_sel), dev), n_sel,
@@ -566,6 +573,7 @@ def ra_paged_decode_attention(q, k_pages, v_pages, page_table, seq_lens, new_len
     return out, lse
 
 
+@functools.lru_cache(maxsize=None)
 def ra_page_select_workspace(B, Hkv, max_pages) -> int:
     n = _lib.ra_page_select_workspace(B, Hkv, max_pages)
     if n == ctypes.c_size_t(-1).value:
@@ -579,23 +587,22 @@ def ra_page_select(q, key_bounds, page_table, seq_lens, n_sel: int, page_size: i
     queries q [B, Tq, Hq, D] (bf16) by the bound that key_bounds
     [n_pages, Hkv, 2, D] puts on a page's scores: int32 [B, Hkv, n_sel],
     ascending, -1 behind.  The new tokens' own pages are always among them."""
-    dev = key_bounds.device
-    if dev.type != "cuda":
+    if not key_bounds.is_cuda:
         raise ValueError("tensors must be contiguous CUDA tensors")
     if q.dim() != 4 or key_bounds.dim() != 4 or page_table.dim() != 2:
         raise ValueError("q must be [B, Tq, Hq, D], key_bounds [n_pages, Hkv, 2, D], page_table [B, max_pages]")
     n_pages, Hkv, _, D = key_bounds.shape
     B, max_pages = page_table.shape
     _, Tq, Hq, _ = q.shape
-    i32 = torch.int32
+    i32, dev = torch.int32, key_bounds.get_device()
     c = ra_paged_cache(None, None, None, None,
                        _expect(key_bounds, "key_bounds", torch.bfloat16, (n_pages, Hkv, 2, D), dev), RA_BF16, n_pages,
                        page_size, Hkv, D, _expect(page_table, "page_table", i32, page_table.shape, dev), B, max_pages,
                        _expect(seq_lens, "seq_lens", i32, (B,), dev), _expect(new_lens, "new_lens", i32, (B,), dev))
     if selected is None:
-        selected = torch.empty((B, Hkv, max(n_sel, 0)), dtype=i32, device=dev)
+        selected = key_bounds.new_empty((B, Hkv, max(n_sel, 0)), dtype=i32)
     if workspace is None:
-        workspace = torch.empty(ra_page_select_workspace(B, Hkv, max_pages), dtype=torch.uint8, device=dev)
+        workspace = key_bounds.new_empty(ra_page_select_workspace(B, Hkv, max_pages), dtype=torch.uint8)
     _call_on(dev, stream, _lib.ra_page_select, "ra_page_select", _expect(q, "q", q.dtype, (B, Tq, Hq, D), dev),
              _dtype_code(q.dtype), ctypes.byref(c), Tq, Hq, n_sel,
              _expect(selected, "selected", i32, (B, Hkv, n_sel), dev), _ptr(workspace),

@@ -69,7 +69,7 @@ __device__ __forceinline__ float e4m3_value(uint32_t c) {
 // remainder x - q s is exact in fp32 (x has 8 significant bits, |x - q s| is at
 // most about s / 2 and a multiple of s's last bit), so the comparison with
 // s / 2 decides every case as infinite precision would.
-__device__ __forceinline__ int quant_i8(float x, float s, float inv) {
+__device__ __forceinline__ uint32_t quant_i8(float x, float s, float inv) {
   float q = rintf(x * inv);
   const float r = fmaf(-q, s, x);
   const float half = 0.5f * s;
@@ -77,51 +77,104 @@ __device__ __forceinline__ int quant_i8(float x, float s, float inv) {
     const float up = r > 0.f ? 1.f : -1.f;
     if (fabsf(r) > half || (static_cast<int>(q) & 1)) q += up;
   }
-  return static_cast<int>(q);
+  return static_cast<uint32_t>(static_cast<int>(q)) & 0xffu;
 }
 
-// The same for e4m3; returns the 8-bit code.  The conversion of x * inv is the
-// answer unless the product lies within a few ulp of a border between two
-// values (the middle of a mantissa step: the low 20 bits of the fp32 are about
-// 0x80000; all of the range below the smallest normal value, 2^-6, is checked);
-// there the exact remainders of the two candidates decide, ties to the even code.
+// The same for e4m3: the conversion of x * inv is the answer or a neighbour of it;
+// the exact remainders of the two candidates decide, ties to the even code.
 __device__ __forceinline__ uint32_t quant_e4m3(float x, float s, float inv) {
-  const float t = fabsf(x) * inv;
+  const float ax = fabsf(x);
   uint16_t pair;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pair) : "f"(0.f), "f"(t));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pair) : "f"(0.f), "f"(ax * inv));
   uint32_t c = pair & 0xffu;
-  const uint32_t low = (__float_as_uint(t) - 0x80000u + 8u) & 0xfffffu;
-  if (low <= 16u || t < 0x1p-6f) {
-    const float ax = fabsf(x);
-    const float r = fmaf(-e4m3_value(c), s, ax);
-    const uint32_t other = r > 0.f ? min(c + 1u, 126u) : (c > 0u ? c - 1u : 0u);
-    const float r2 = fabsf(fmaf(-e4m3_value(other), s, ax)), r1 = fabsf(r);
-    if (r2 < r1 || (r2 == r1 && (c & 1u))) c = other;
-  }
+  const float r = fmaf(-e4m3_value(c), s, ax);
+  const uint32_t other = r > 0.f ? min(c + 1u, 126u) : (c > 0u ? c - 1u : 0u);
+  const float r2 = fabsf(fmaf(-e4m3_value(other), s, ax)), r1 = fabsf(r);
+  if (r2 < r1 || (r2 == r1 && (c & 1u))) c = other;
   return c | (x < 0.f ? 0x80u : 0u);
 }
 
-// Eight cached values (8 codes of one row, or 8 bf16) as fp32.
+__device__ __forceinline__ uint32_t e4m3_quad(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+      "mov.b32 %0, {l, h};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
+// Eight bf16 values (pairs in u) of a row with scale s as codes.  Nearly all octets
+// have no value near a border between two codes; those take the short way:
+//   int8: x * inv + 1.5 2^23 in one fma rounds the product to the integer in the
+//   sum's low bits (the conversion instructions run at a quarter of the fma
+//   rate); the exact remainders of all eight must stay below s / 2.
+//   e4m3: with inv within 2^-22 of 1 / s, x (1 - 2^-21) inv and x (1 + 2^-21) inv lie
+//   on either side of x / s even after their own rounding; the conversion is
+//   monotonic, so where both give the same code it is the quotient's.
+// The others go value by value.
 template <int ET>
-__device__ __forceinline__ void cached_octet(const void* pages, long long index, float scale, float (&v)[8]) {
-  if constexpr (ET == kCacheBf16) {
-    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(pages) + index);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ uint2 quant_octet(const uint32_t (&u)[4], float s, float inv) {
+  float x[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-  } else {
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pages) + index);
-    const uint32_t u[2] = {w.x, w.y};
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(u[i] << 16);
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+  uint32_t code[2];
+  bool plain;
+  if constexpr (ET == kCacheI8) {
+    uint32_t y[8];
+    float worst = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t c = (u[i >> 2] >> (8 * (i & 3))) & 0xffu;
-      if constexpr (ET == kCacheI8) v[i] = static_cast<float>(static_cast<int8_t>(c)) * scale;
-      else v[i] = __uint_as_float(__float_as_uint(e4m3_value(c & 0x7fu)) | ((c & 0x80u) << 24)) * scale;
+      const float t = fmaf(x[i], inv, 12582912.f);
+      y[i] = __float_as_uint(t);
+      worst = fmaxf(worst, fabsf(fmaf(-(t - 12582912.f), s, x[i])));
     }
+    plain = worst < 0.5f * s;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      code[i] = __byte_perm(__byte_perm(y[4 * i], y[4 * i + 1], 0x0040), __byte_perm(y[4 * i + 2], y[4 * i + 3], 0x0040), 0x5410);
+  } else {
+    const float below = inv * (1.f - 0x1p-21f), above = inv * (1.f + 0x1p-21f);
+    uint32_t differ = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      code[i] = e4m3_quad(x[4 * i] * below, x[4 * i + 1] * below, x[4 * i + 2] * below, x[4 * i + 3] * below);
+      differ |= code[i] ^ e4m3_quad(x[4 * i] * above, x[4 * i + 1] * above, x[4 * i + 2] * above, x[4 * i + 3] * above);
+    }
+    plain = differ == 0u;
   }
+  if (!plain) {
+    code[0] = code[1] = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      code[i >> 2] |= (ET == kCacheI8 ? quant_i8(x[i], s, inv) : quant_e4m3(x[i], s, inv)) << (8 * (i & 3));
+  }
+  return make_uint2(code[0], code[1]);
+}
+
+// Eight bf16 values as fp32.
+__device__ __forceinline__ void bf16_octet(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 w = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+
+// Of pairs; a NaN yields to the other operand.
+__device__ __forceinline__ uint32_t bf16x2_min(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // ------------------------------------------------------------------- append
@@ -141,7 +194,19 @@ struct AppendArgs {
 };
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendBatch = 4;  // rows of K and V a lane holds in flight
+constexpr int kAppendBatch = 2;  // rows of K and V a lane holds in flight
+
+// fp32(a / m), m = 127 or 448, for a >= 2^-100 with 8 significant bits, by the
+// division with a divisor known in advance of Brisebarre, Muller and Raina (IEEE
+// Trans. Computers 2004): the product with the rounded 1 / m, its exact
+// remainder, and the remainder's product added back.  That it is the correctly
+// rounded quotient for every such a is checked value by value in the tests.
+template <int ET>
+__device__ __forceinline__ float scale_of(float a) {
+  constexpr float m = ET == kCacheI8 ? 127.f : 448.f, r = static_cast<float>(1.0 / m);
+  const float q = a * r;
+  return fmaf(fmaf(-q, m, a), r, q);
+}
 
 // One row's octet of this lane into the cache: bits, or codes and the row's
 // scale (largest magnitude over the LPR lanes of the row).  bf16 magnitudes
@@ -164,20 +229,13 @@ __device__ __forceinline__ void append_row(const uint4& w, bool act, int lane_in
     if (am >= 0x7f80u) {
       s = __uint_as_float(0x7fc00000u);  // NaN: the row reads back as NaN
     } else if (__uint_as_float(am << 16) >= 0x1p-100f) {
-      s = __fdiv_rn(__uint_as_float(am << 16), ET == kCacheI8 ? 127.f : 448.f);
-      inv = 1.f / s;
+      s = scale_of<ET>(__uint_as_float(am << 16));
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));  // near enough: see quant_octet
     }
-    uint32_t code[2] = {0u, 0u};
-    if (inv != 0.f) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x = __uint_as_float((i & 1) ? (u[i >> 1] & 0xffff0000u) : (u[i >> 1] << 16));
-        const uint32_t c = ET == kCacheI8 ? static_cast<uint32_t>(quant_i8(x, s, inv)) & 0xffu : quant_e4m3(x, s, inv);
-        code[i >> 2] |= c << (8 * (i & 3));
-      }
-    }
+    uint2 code = make_uint2(0u, 0u);
+    if (inv != 0.f) code = quant_octet<ET>(u, s, inv);
     if (act) {
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pages) + row * D + 8 * lane_in_row) = make_uint2(code[0], code[1]);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pages) + row * D + 8 * lane_in_row) = code;
       if (lane_in_row == 0) scales[row] = s;
     }
   }
@@ -189,9 +247,9 @@ __device__ __forceinline__ void append_row(const uint4& w, bool act, int lane_in
 // warp and step, kAppendBatch steps' loads in flight.  The column minima and
 // maxima of the keys stay in registers until the unit's end.
 template <int D, int ET>
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
-  __shared__ float s_lo[kAppendThreads / 32][D], s_hi[kAppendThreads / 32][D];
+  __shared__ uint32_t s_lo[kAppendThreads / 32][D / 2], s_hi[kAppendThreads / 32][D / 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / LPR, lr = lane % LPR;
   const int upc = (kAppendThreads / 32) / a.wpu, wi = warp % a.wpu;  // units per CTA, warp in the unit
@@ -214,12 +272,9 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
       tok0 = static_cast<int>(first) - begin;  // token of the page's row 0 (may be negative)
     }
   }
-  float lo[8], hi[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo[i] = INFINITY;
-    hi[i] = -INFINITY;
-  }
+  // pairs of columns; min and max of bf16 pass over a NaN
+  uint32_t lo[4] = {0x7f807f80u, 0x7f807f80u, 0x7f807f80u, 0x7f807f80u};
+  uint32_t hi[4] = {0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u};
   if (page >= 0) {
     const long long prow = (static_cast<long long>(page) * a.bt.Hkv + h) << a.bt.page_shift;
     const int step = a.wpu * RPW;
@@ -245,10 +300,9 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
         if (a.bounds && act) {
           const uint32_t w[4] = {kw[u].x, kw[u].y, kw[u].z, kw[u].w};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {  // fminf and fmaxf pass over a NaN
-            const float x = __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
-            lo[i] = fminf(lo[i], x);
-            hi[i] = fmaxf(hi[i], x);
+          for (int i = 0; i < 4; ++i) {
+            lo[i] = bf16x2_min(lo[i], w[i]);
+            hi[i] = bf16x2_max(hi[i], w[i]);
           }
         }
       }
@@ -256,44 +310,41 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
   }
   if (a.bounds == nullptr) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int o = LPR; o < 32; o <<= 1) {
-      lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
-      hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+      lo[i] = bf16x2_min(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+      hi[i] = bf16x2_max(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
     }
   if (a.wpu > 1) {
     if (sub == 0)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s_lo[warp][8 * lr + i] = lo[i];
-        s_hi[warp][8 * lr + i] = hi[i];
+      for (int i = 0; i < 4; ++i) {
+        s_lo[warp][4 * lr + i] = lo[i];
+        s_hi[warp][4 * lr + i] = hi[i];
       }
     __syncthreads();
     if (wi == 0)
       for (int w = 1; w < a.wpu; ++w)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          lo[i] = fminf(lo[i], s_lo[warp + w][8 * lr + i]);
-          hi[i] = fmaxf(hi[i], s_hi[warp + w][8 * lr + i]);
+        for (int i = 0; i < 4; ++i) {
+          lo[i] = bf16x2_min(lo[i], s_lo[warp + w][4 * lr + i]);
+          hi[i] = bf16x2_max(hi[i], s_hi[warp + w][4 * lr + i]);
         }
   }
   if (page < 0 || wi != 0 || sub != 0) return;
-  __nv_bfloat16* bl = a.bounds + (static_cast<long long>(page) * a.bt.Hkv + h) * 2 * D + 8 * lr;
+  uint4* bl = reinterpret_cast<uint4*>(a.bounds + (static_cast<long long>(page) * a.bt.Hkv + h) * 2 * D) + lr;
   if (r0 > 0) {  // earlier tokens' bounds stand in the page
-    float old[8];
-    cached_octet<kCacheBf16>(bl, 0, 1.f, old);
+    const uint4 x = bl[0], y = bl[D / 8];
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) lo[i] = fminf(lo[i], old[i]);
-    cached_octet<kCacheBf16>(bl, D, 1.f, old);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) hi[i] = fmaxf(hi[i], old[i]);
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = bf16x2_min(lo[i], xs[i]);
+      hi[i] = bf16x2_max(hi[i], ys[i]);
+    }
   }
-  // the bounds are bf16 values (or infinities) already: packing them is exact
-  *reinterpret_cast<uint4*>(bl) = make_uint4(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]),
-                                             pack_bf16x2(lo[4], lo[5]), pack_bf16x2(lo[6], lo[7]));
-  *reinterpret_cast<uint4*>(bl + D) = make_uint4(pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3]),
-                                                 pack_bf16x2(hi[4], hi[5]), pack_bf16x2(hi[6], hi[7]));
+  bl[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  bl[D / 8] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
 }
 
 // --------------------------------------------------------------------- read
@@ -310,8 +361,56 @@ struct ReadArgs {
 
 constexpr int kReadRows = 16;  // output rows of a warp
 
+// One row's octet of a lane as it is stored, with its scale, and as fp32 values.
+template <int ET>
+struct Octet {
+  uint4 w;  // (8-bit codes: x and y)
+  float scale;
+};
+template <int ET>
+__device__ __forceinline__ Octet<ET> load_octet(const void* pages, const float* scales, long long row, int D, int col) {
+  Octet<ET> o;
+  o.w = make_uint4(0u, 0u, 0u, 0u);
+  o.scale = 0.f;
+  if (row < 0) return o;
+  if constexpr (ET == kCacheBf16) {
+    o.w = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(pages) + row * D + col));
+  } else {
+    const uint2 c = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pages) + row * D + col));
+    o.w.x = c.x;
+    o.w.y = c.y;
+    o.scale = scales[row];
+  }
+  return o;
+}
+template <int ET>
+__device__ __forceinline__ void octet_values(const Octet<ET>& o, float (&v)[8]) {
+  if constexpr (ET == kCacheBf16) {
+    const uint32_t u[4] = {o.w.x, o.w.y, o.w.z, o.w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  } else {
+    const uint32_t u[2] = {o.w.x, o.w.y};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (ET == kCacheI8) {
+        // 2^23 + 128 + code as an fp32's bits (the byte with its sign flipped), less 2^23 + 128
+        const uint32_t c = __byte_perm(u[i >> 2] ^ 0x80808080u, 0x4b000000u, 0x7650 + (i & 3));
+        v[i] = (__uint_as_float(c) - 8388736.f) * o.scale;
+      } else {
+        const uint32_t c = (u[i >> 2] >> (8 * (i & 3))) & 0xffu;
+        v[i] = __uint_as_float(__float_as_uint(e4m3_value(c & 0x7fu)) | ((c & 0x80u) << 24)) * o.scale;
+      }
+    }
+  }
+}
+
 // A warp takes 16 consecutive tokens of one KV head (runs of 16 rows of a page
-// to read, heads side by side in the CTA to write); D / 8 lanes hold a row.
+// to read, heads side by side in the CTA to write); D / 8 lanes hold a row.  Keys
+// and values of all 16 are loaded before the first is written.
 template <int D, int ET, typename Tout>
 __global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int LPR = D / 8, RPW = 32 / LPR, N = kReadRows / RPW;
@@ -323,41 +422,47 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__
   const long long bg = unit / a.bt.Hkv;
   const int g = static_cast<int>(bg % a.groups), b = static_cast<int>(bg / a.groups);
   const int t0 = g * kReadRows;
+  // lane i < 16: the cache row of output row t0 + i, -1 where there is none.  The
+  // table entry is loaded beside the length that says whether it counts.
+  const long long pos = static_cast<long long>(a.first) + t0 + (lane & (kReadRows - 1));
+  const long long logical = min(pos >> a.bt.page_shift, static_cast<long long>(a.bt.max_pages - 1));
+  const int page = a.bt.page_table[static_cast<long long>(b) * a.bt.max_pages + logical];
   const int len = seq_len_of(a.bt, b).len;
-  // lane i < 16: the cache row of output row t0 + i, -1 where there is none
   long long mine = -1;
-  const long long pos = static_cast<long long>(a.first) + t0 + lane;
   if (lane < kReadRows && pos < len) {
-    const int page = page_of(a.bt, b, static_cast<int>(pos >> a.bt.page_shift));
-    if (page >= 0)
+    if (page >= 0 && page < a.bt.n_pages)
       mine = ((static_cast<long long>(page) * a.bt.Hkv + h) << a.bt.page_shift) + (pos & ((1 << a.bt.page_shift) - 1));
+    else
+      set_status(RA_ERR_DEVICE_BOUNDS);
   }
+  Octet<ET> o[2][N];
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    if (a.out[kv] == nullptr) continue;
-    float v[N][8];
+  for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const long long row = __shfl_sync(0xffffffffu, mine, i * RPW + sub);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-      if (row >= 0) {
-        const float s = ET == kCacheBf16 ? 1.f : a.scales[kv][row];
-        cached_octet<ET>(a.pages[kv], row * D + 8 * lr, s, v[i]);
-      }
+      o[kv][i] = load_octet<ET>(a.pages[kv], a.scales[kv], a.out[kv] ? row : -1, D, 8 * lr);
     }
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    if (a.out[kv] == nullptr) continue;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int t = t0 + i * RPW + sub;
       if (t >= a.bt.T) continue;
       Tout* dst = static_cast<Tout*>(a.out[kv]) + ((static_cast<long long>(b) * a.bt.T + t) * a.bt.Hkv + h) * D + 8 * lr;
-      if constexpr (sizeof(Tout) == 2) {
-        __stcs(reinterpret_cast<uint4*>(dst),
-               make_uint4(pack_bf16x2(v[i][0], v[i][1]), pack_bf16x2(v[i][2], v[i][3]), pack_bf16x2(v[i][4], v[i][5]),
-                          pack_bf16x2(v[i][6], v[i][7])));
+      if constexpr (sizeof(Tout) == 2 && ET == kCacheBf16) {
+        __stcs(reinterpret_cast<uint4*>(dst), o[kv][i].w);
       } else {
-        __stcs(reinterpret_cast<float4*>(dst), make_float4(v[i][0], v[i][1], v[i][2], v[i][3]));
-        __stcs(reinterpret_cast<float4*>(dst) + 1, make_float4(v[i][4], v[i][5], v[i][6], v[i][7]));
+        float v[8];
+        octet_values<ET>(o[kv][i], v);
+        if constexpr (sizeof(Tout) == 2) {
+          __stcs(reinterpret_cast<uint4*>(dst),
+                 make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+        } else {
+          __stcs(reinterpret_cast<float4*>(dst), make_float4(v[0], v[1], v[2], v[3]));
+          __stcs(reinterpret_cast<float4*>(dst) + 1, make_float4(v[4], v[5], v[6], v[7]));
+        }
       }
     }
   }

@@ -251,12 +251,18 @@ __device__ __forceinline__ void pg_store2(const PagedArgs& a, long long row, int
 
 // ------------------------------------------------------------------ walker
 
+// x / y of values that are not negative; most fit 32 bits, where a division is much shorter.
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return static_cast<unsigned>(x) / static_cast<unsigned>(y);
+  return x / y;
+}
+
 // The walker warp: lane t < teams walks the run of team t.  In every round the
 // lanes whose queue has room post one tile.  Page numbers are loaded when a
 // tile is reached and used in the round that posts it, so their latency
-// overlaps the rounds between.
+// overlaps the rounds between.  len0: the length of sequence `lane`.
 template <int D, int ET, int NB>
-__device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volatile int* abort_flag) {
+__device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volatile int* abort_flag, int len0) {
   using SL = PgSmem<D, ET, NB>;
   const int lane = threadIdx.x & 31;
   const int teams = SL::kWarps / a.R;
@@ -265,17 +271,20 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
   PgTile* queue = reinterpret_cast<PgTile*>(smem + SL::kMeta) + kPgQueue * lane;
   const int ps = 1 << a.bt.page_shift;
 
-  // the line and this lane's run [f0, f1) of it
-  long long total = 0;
-  for (int b = lane; b < a.bt.B; b += 32) total += pg_units(a, seq_len_of(a.bt, b).len);
+  // the line and this lane's run [f0, f0 + n) of it; lane i holds the units of sequence i of each 32
+  long long total = 0, own = 0;
+  for (int i = lane; i < a.bt.B; i += 32) {
+    own = pg_units(a, i == lane ? len0 : seq_len_of(a.bt, i).len);
+    total += own;
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const long long U = static_cast<long long>(gridDim.x) * teams;
   const long long u = static_cast<long long>(lane) * gridDim.x + blockIdx.x;
-  long long run = (total + U - 1) / U;
-  if (run < a.min_run) run = a.min_run;
-  const long long f0 = u * run, f1 = min(f0 + run, total);
-  bool work = lane < teams && f0 < f1;
+  const int run = max(static_cast<int>(quotient(total + U - 1, U)), a.min_run);  // (below 2^30: the host bounds the line)
+  const long long f0 = u * run;
+  const int n = static_cast<int>(max(min(f0 + run, total) - f0, 0ll));
+  bool work = lane < teams && n > 0;
   // its place: sequence b (starting at unit `start` of the line)
   int b = 0;
   long long start = 0;
@@ -283,21 +292,22 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
     long long before = 0;
     bool found = false;
     for (int b0 = 0; b0 < a.bt.B; b0 += 32) {
-      long long upto = b0 + lane < a.bt.B ? pg_units(a, seq_len_of(a.bt, b0 + lane).len) : 0;
+      if (a.bt.B > 32) own = b0 + lane < a.bt.B ? pg_units(a, seq_len_of(a.bt, b0 + lane).len) : 0;
+      long long upto = b0 + lane < a.bt.B ? own : 0;
       const long long mine = upto;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += x;
       }
-      const int n = min(32, a.bt.B - b0);
-      for (int i = 0; i < n; ++i) {
+      const int m = min(32, a.bt.B - b0);
+      for (int i = 0; i < m; ++i) {
         const long long e = before + __shfl_sync(0xffffffffu, upto, i);
-        const long long s = e - __shfl_sync(0xffffffffu, mine, i);
+        const long long x = e - __shfl_sync(0xffffffffu, mine, i);
         if (work && !found && f0 < e) {
           found = true;
           b = b0 + i;
-          start = s;
+          start = x;
         }
       }
       before += __shfl_sync(0xffffffffu, upto, 31);
@@ -305,22 +315,22 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
   }
   SeqLen s = {0, 0};
   int nt = 0, h = 0, t = 0;
-  long long pair0 = 0;  // the pair's first unit on the line
+  int pair = 0;  // the pair's first unit, from f0 (negative where an earlier team began it)
   if (work) {
     s = seq_len_of(a.bt, b);
     nt = pg_tiles(a, s.len);
     const long long rel = f0 - start;
-    h = static_cast<int>(rel / (nt + kPgPairCost));
-    pair0 = start + static_cast<long long>(h) * (nt + kPgPairCost);
-    t = max(static_cast<int>(f0 - pair0) - kPgPairCost, 0);
+    h = static_cast<int>(quotient(rel, nt + kPgPairCost));
+    pair = static_cast<int>(static_cast<long long>(h) * (nt + kPgPairCost) - rel);
+    t = max(-pair - kPgPairCost, 0);
   }
   // the next tile with work at or behind (b, h, t); work = false behind the run's end
   auto settle = [&]() {
     while (work) {
-      if (pair0 + kPgPairCost + t >= f1) work = false;  // the rest of the line is other teams'
+      if (pair + kPgPairCost + t >= n) work = false;  // the rest of the line is other teams'
       else if (t < nt) break;
       else {
-        pair0 += nt + kPgPairCost;
+        pair += nt + kPgPairCost;
         t = 0;
         if (++h == a.bt.Hkv) {
           h = 0;
@@ -396,13 +406,13 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
           m.r1 = m.r0 + 16;
           m.p1 = m.p0 + 16;
         }
-        const bool owner = pair0 + kPgPairCost >= f0;
-        const bool last = t + 1 == nt || pair0 + kPgPairCost + t + 1 >= f1;
+        const bool owner = pair + kPgPairCost >= 0;
+        const bool last = t + 1 == nt || pair + kPgPairCost + t + 1 >= n;
         flags = (first ? kPgFirst : 0) | (last ? kPgLast : 0) | (owner && t + 1 == nt ? kPgWhole : 0) | (owner ? kPgOwner : 0);
         if (first && owner) {  // the pair's record: cut, if its last tile is another team's
-          const long long ul = (pair0 + kPgPairCost + nt - 1) / run;
+          const int on = static_cast<int>(static_cast<unsigned>(pair + kPgPairCost + nt - 1) / static_cast<unsigned>(run));
           a.cut[static_cast<long long>(b) * a.bt.Hkv + h] =
-              ul == u ? make_int2(-1, -1) : make_int2(static_cast<int>(u), static_cast<int>(ul));
+              on == 0 ? make_int2(-1, -1) : make_int2(static_cast<int>(u), static_cast<int>(u) + on);
         }
         first = last;
         ++t;
@@ -453,6 +463,8 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB>::kThreads, 1)
 
   // the combine kernel may be brought onto the SMs; it waits for this grid's end itself
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int len0 = 0;  // the walker's first lengths, on their way while the barriers are set up
+  if (warp == SL::kWarps && lane < a.bt.B) len0 = seq_len_of(a.bt, lane).len;
   if (tid == 32 * SL::kWarps) *abort_flag = grid_timed_out() ? 1 : 0;
   for (int i = tid; i < teams * slots; i += SL::kThreads) {
     mbar_init(sb + SL::kFull + 8u * i, 32 * a.R);  // every thread of the team
@@ -466,7 +478,7 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB>::kThreads, 1)
   __syncthreads();
   if (*abort_flag) return;
   if (warp == SL::kWarps) {
-    pg_walk<D, ET, NB>(a, smem, abort_flag);
+    pg_walk<D, ET, NB>(a, smem, abort_flag, len0);
     return;
   }
 

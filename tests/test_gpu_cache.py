@@ -146,6 +146,24 @@ def test_append_rounds_as_exact_arithmetic(cuda_lib, dtype, D):
     assert ra.ra_get_device_status() == ra.RA_OK
 
 
+@pytest.mark.parametrize("dtype", ["int8", "e4m3"])
+def test_every_scale_is_correctly_rounded(cuda_lib, dtype):
+    """All bf16 magnitudes from 2^-100 up as a row's largest value."""
+    ra = cuda_lib
+    bits = torch.arange(27 << 7, 0x7f80, dtype=torch.int32).to(torch.int16)  # 2^-100 ... the largest finite
+    amax = bits.view(torch.bfloat16)
+    D, ps, T = 64, 128, len(bits)
+    k = torch.zeros((1, T, 1, D), dtype=torch.bfloat16)
+    k[0, :, 0, 17] = amax
+    table = torch.arange(-(-T // ps), dtype=torch.int32)[None].contiguous()
+    dev = Device(table.numel(), 1, ps, D, dtype, bounds=False)
+    ra.ra_cache_append(k.cuda(), -k.cuda(), dev.k, dev.v, table.cuda(), torch.tensor([T], dtype=torch.int32).cuda(), **dev.kw())
+    want = (amax.double() / P.QMAX[dtype]).float()  # (no such quotient is near a tie of fp32: its bits repeat)
+    for s in (dev.ks, dev.vs):
+        assert torch.equal(s.cpu().view(-1)[:T], want)
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "int8", "e4m3"])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("B,Hkv,D,ps,seq,first,T", [
