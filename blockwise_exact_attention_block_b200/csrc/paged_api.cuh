@@ -100,12 +100,12 @@ PagedPlan paged_plan(int B, int Tq, int Hq, int Hkv, int D) {
   return p;
 }
 
-template <int D, int WPR, int NW>
+template <int D, int COLS, int WPR, int NW>
 ra_status launch_paged_combine(const PagedArgs& a, int teams, cudaStream_t st) {
   const long long rows = static_cast<long long>(a.bt.B) * a.bt.Hkv * a.rows;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + NW / WPR - 1) / (NW / WPR)), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + NW / WPR - 1) / (NW / WPR) * (D / COLS)), 1, 1);
   cfg.blockDim = dim3(32 * NW, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -113,7 +113,7 @@ ra_status launch_paged_combine(const PagedArgs& a, int teams, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, WPR, NW>, a, teams));
+  return cuda_status(cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, COLS, WPR, NW>, a, teams));
 }
 
 template <int D, int ET, int NB>
@@ -140,9 +140,9 @@ ra_status launch_paged_t(const PagedArgs& a, cudaStream_t st) {
   // a row's parts: 32 warps where the rows are few, one where they alone fill the GPU
   const long long rows = static_cast<long long>(a.bt.B) * a.bt.Hkv * a.rows;
   const int teams = grid * (SL::kWarps / a.R);
-  if (rows <= 2 * sm_count()) return launch_paged_combine<D, 32, 32>(a, teams, st);
-  if (rows <= 16 * sm_count()) return launch_paged_combine<D, 8, 8>(a, teams, st);
-  return launch_paged_combine<D, 1, 8>(a, teams, st);
+  if (rows * (D / 32) <= sm_count()) return launch_paged_combine<D, 32, 32, 32>(a, teams, st);
+  if (rows <= 16 * sm_count()) return launch_paged_combine<D, D, 8, 8>(a, teams, st);
+  return launch_paged_combine<D, D, 1, 8>(a, teams, st);
 }
 
 template <int D, int ET>

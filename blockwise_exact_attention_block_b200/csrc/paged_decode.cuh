@@ -932,17 +932,20 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB>::kThreads, 1)
 }
 
 // Joins the parts of the cut pairs: with M = max E_i over the parts,
-// l = sum 2^(E_i - M) l_i, out = sum 2^(E_i - M) o_i / l.  WPR warps of a CTA of
-// NW share a row; the lanes hold its D columns.  32 to a row where rows are few
-// and their parts many (592 for one token against 1M keys), one where the rows
-// alone fill the GPU.  Every part is read once and in a fixed order: the result
-// does not depend on scheduling.
-template <int D, int WPR, int NW>
+// l = sum 2^(E_i - M) l_i, out = sum 2^(E_i - M) o_i / l.  A CTA of NW warps does
+// `COLS` columns of NW / WPR rows, WPR warps to a row, each with every WPR-th part.
+// Where rows are few and their parts many (592 for one token against 1M keys),
+// 32 warps share a row and the row's columns are spread over CTAs, 32 to each: a
+// warp's parts then fit one or two batches of loads.  Where the rows alone
+// fill the GPU a warp does a whole one.  Every part is read once and in a fixed
+// order: the result does not depend on scheduling.
+template <int D, int COLS, int WPR, int NW>
 __global__ void __launch_bounds__(32 * NW) paged_combine_kernel(const __grid_constant__ PagedArgs a, int max_teams) {
-  constexpr int kPer = D / 32, kBatch = NW == 32 ? 4 : 8;
-  __shared__ float s_acc[WPR == 1 ? 1 : NW][D], s_l[NW], s_m[NW];
+  constexpr int kPer = COLS / 32, kBatch = WPR == 32 ? 8 : 16 / kPer;
+  __shared__ float s_acc[WPR == 1 ? 1 : NW][COLS], s_l[NW], s_m[NW];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long id = static_cast<long long>(blockIdx.x) * (NW / WPR) + warp / WPR;
+  const int col = COLS * (blockIdx.x % (D / COLS)) + kPer * lane;
+  const long long id = static_cast<long long>(blockIdx.x / (D / COLS)) * (NW / WPR) + warp / WPR;
   const int w0 = warp % WPR;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long pairs = static_cast<long long>(a.bt.B) * a.bt.Hkv;
@@ -967,7 +970,7 @@ __global__ void __launch_bounds__(32 * NW) paged_combine_kernel(const __grid_con
       for (int e = 0; e < kPer; ++e) v[k][e] = 0.f;
       if (t <= cut.y) {
         ml[k] = a.part_ml[part(t)];
-        const float* src = a.part_o + part(t) * D + kPer * lane;
+        const float* src = a.part_o + part(t) * D + col;
 #pragma unroll
         for (int e = 0; e < kPer; ++e) v[k][e] = src[e];
       }
@@ -1022,10 +1025,13 @@ __global__ void __launch_bounds__(32 * NW) paged_combine_kernel(const __grid_con
   const float inv = has ? 1.f / L : 0.f;
   const int b = static_cast<int>(pair / a.bt.Hkv), h = static_cast<int>(pair % a.bt.Hkv);
   const long long row = (static_cast<long long>(b) * a.bt.T + r / a.groups) * a.Hq + h * a.groups + r % a.groups;
+  if constexpr (kPer == 1)
+    pg_store1(a, row, D, col, has ? acc[0] * inv : 0.f);
+  else
 #pragma unroll
-  for (int e = 0; e < kPer; e += 2)
-    pg_store2(a, row, D, kPer * lane + e, has ? acc[e] * inv : 0.f, has ? acc[e + 1] * inv : 0.f);
-  if (lane == 0) a.lse[row] = has ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+    for (int e = 0; e < kPer; e += 2)
+      pg_store2(a, row, D, col + e, has ? acc[e] * inv : 0.f, has ? acc[e + 1] * inv : 0.f);
+  if (lane == 0 && col == 0) a.lse[row] = has ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
 }  // namespace ra
