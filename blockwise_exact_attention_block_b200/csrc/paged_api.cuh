@@ -116,14 +116,14 @@ ra_status launch_paged_combine(const PagedArgs& a, int teams, cudaStream_t st) {
   return cuda_status(cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, COLS, WPR, NW>, a, teams));
 }
 
-template <int D, int ET, int NB>
+template <int D, int ET, int NB, bool TEAMS>
 ra_status launch_paged_t(const PagedArgs& a, cudaStream_t st) {
-  using SL = PgSmem<D, ET, NB>;
+  using SL = PgSmem<D, ET, NB, TEAMS>;
   static int attr_set[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 64 || !attr_set[dev]) {
-    if (cudaFuncSetAttribute(paged_partial_kernel<D, ET, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(paged_partial_kernel<D, ET, NB, TEAMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              SL::kBytes) != cudaSuccess)
       return RA_ERR_CUDA;
     if (dev < 64) attr_set[dev] = 1;
@@ -134,7 +134,7 @@ ra_status launch_paged_t(const PagedArgs& a, cudaStream_t st) {
   const long long line = (tiles + kPgPairCost) * a.bt.B * a.bt.Hkv;
   const long long runs = (line + a.min_run - 1) / a.min_run;
   const int grid = static_cast<int>(runs < sm_count() ? runs : sm_count());
-  paged_partial_kernel<D, ET, NB><<<grid, SL::kThreads, SL::kBytes, st>>>(a);
+  paged_partial_kernel<D, ET, NB, TEAMS><<<grid, SL::kThreads, SL::kBytes, st>>>(a);
   const ra_status s = cuda_status(cudaGetLastError());
   if (s != RA_OK) return s;
   // a row's parts: 32 warps where the rows are few, one where they alone fill the GPU
@@ -147,7 +147,8 @@ ra_status launch_paged_t(const PagedArgs& a, cudaStream_t st) {
 
 template <int D, int ET>
 ra_status launch_paged_e(const PagedArgs& a, cudaStream_t st) {
-  return a.rows <= 8 ? launch_paged_t<D, ET, 1>(a, st) : launch_paged_t<D, ET, 2>(a, st);
+  if (a.rows <= 8) return launch_paged_t<D, ET, 1, false>(a, st);
+  return a.R == 1 ? launch_paged_t<D, ET, 2, false>(a, st) : launch_paged_t<D, ET, 2, true>(a, st);
 }
 
 template <int D>

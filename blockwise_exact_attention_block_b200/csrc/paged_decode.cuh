@@ -92,17 +92,21 @@ struct PagedArgs {
   float* lse;
 };
 
-// Shared memory and the shape of a CTA.  bf16: 8 consumer warps with rings of
-// 24 KB keep the copies in flight that HBM needs.  An 8-bit tile has half the
-// bytes and a conversion of its codes besides, so instruction issue is what
-// must be fed: 15 warps of 8 rows (128 registers), 11 of 16 rows (168: the
-// output accumulators alone take 64).  With the producer that is a multiple of
-// four warps, which the register file is shared out by.
-template <int D, int ET, int NB>
+// Shared memory and the shape of a CTA, the walker's warp included a multiple of
+// four warps where registers matter (the register file is shared out by four).
+// bf16, D = 128: an item is 8 KB, and 8 consumer warps with rings of three keep
+// the copies in flight that HBM needs; 16 rows each want 255 registers, so 7 there
+// (99 us against 117 with 8 and spilled registers: 8 x 9k-24k keys, 16 rows), but 8
+// for teams of several warps, which 7 would leave with one team of four.  Smaller
+// items, and a conversion of 8-bit codes besides, make instruction issue what
+// must be fed: 15 warps of 8 rows (128 registers), 11 of 16 rows (168: the output
+// accumulators alone take 64).
+template <int D, int ET, int NB, bool TEAMS>
 struct PgSmem {
-  static constexpr int kWarps = ET == kCacheBf16 ? 8 : NB == 1 ? 15 : 11;
+  static constexpr bool kWide = ET == kCacheBf16 && D == 128;  // items of 8 KB
+  static constexpr int kWarps = kWide ? (NB == 1 || TEAMS ? 8 : 7) : NB == 1 ? 15 : 11;
   static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kRing = ET == kCacheBf16 ? 24576 : NB == 1 ? 12288 : 16384;  // bytes per warp
+  static constexpr int kRing = kWide ? 24576 : NB == 1 ? 12288 : 16384;  // bytes per warp
   static constexpr int kElem = ET == kCacheBf16 ? 2 : 1;
   static constexpr int kItem = kPgKeys * D * kElem;  // one tile of K or of V
   static constexpr int kSlots = kRing / kItem < kPgSlots ? kRing / kItem : kPgSlots;  // per warp
@@ -261,9 +265,9 @@ __device__ __forceinline__ long long quotient(long long x, long long y) {
 // lanes whose queue has room post one tile.  Page numbers are loaded when a
 // tile is reached and used in the round that posts it, so their latency
 // overlaps the rounds between.  len0: the length of sequence `lane`.
-template <int D, int ET, int NB>
+template <int D, int ET, int NB, bool TEAMS>
 __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volatile int* abort_flag, int len0) {
-  using SL = PgSmem<D, ET, NB>;
+  using SL = PgSmem<D, ET, NB, TEAMS>;
   const int lane = threadIdx.x & 31;
   const int teams = SL::kWarps / a.R;
   const uint32_t sb = smem_u32(smem);
@@ -447,10 +451,10 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
 
 // ---------------------------------------------------------------- consumers
 
-template <int D, int ET, int NB>
-__global__ void __launch_bounds__(PgSmem<D, ET, NB>::kThreads, 1)
+template <int D, int ET, int NB, bool TEAMS>
+__global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
     paged_partial_kernel(const __grid_constant__ PagedArgs a) {
-  using SL = PgSmem<D, ET, NB>;
+  using SL = PgSmem<D, ET, NB, TEAMS>;
   constexpr int KS = D / 16;  // k16 steps of the score product, and 16-column blocks of the output
   constexpr int NR = 2 * NB;  // query rows of a lane: 8 nb + 2 (lane % 4), + 1
   constexpr int ROW = SL::kRow;
@@ -478,7 +482,7 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB>::kThreads, 1)
   __syncthreads();
   if (*abort_flag) return;
   if (warp == SL::kWarps) {
-    pg_walk<D, ET, NB>(a, smem, abort_flag, len0);
+    pg_walk<D, ET, NB, TEAMS>(a, smem, abort_flag, len0);
     return;
   }
 
@@ -517,11 +521,11 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB>::kThreads, 1)
   uint32_t lphase = 0, lqphase = 0;
   bool lstop = false, wrapped = false, ok = true;
   auto copy_item = [&](const uint8_t* src, const float* sc) {
-    if (a.R > 1 && wrapped) ok &= mbar_wait(empty + 8u * lslot, lphase ^ 1u, abort_flag);  // (one warp: it has read the slot)
+    if (TEAMS && wrapped) ok &= mbar_wait(empty + 8u * lslot, lphase ^ 1u, abort_flag);  // (one warp: it has read the slot)
     const uint8_t* g0 = src + static_cast<long long>(lr0) * ROW;
     const uint8_t* g1 = src + static_cast<long long>(lr1) * ROW - SL::kItem / 2;
     const uint32_t dst = ring + lslot * SL::kItem;
-    if (a.R == 1) {
+    if (!TEAMS) {
       uint32_t d[kFlips];
 #pragma unroll
       for (int i = 0; i < kFlips; ++i) d[i] = dst + (lane_off ^ (static_cast<uint32_t>(512 / ROW * i & 7) << 4));
@@ -563,7 +567,7 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB>::kThreads, 1)
   uint32_t phase = 0;
   auto release = [&]() {  // this warp has read the slot
     __syncwarp();
-    if (a.R > 1 && lane == 0) mbar_arrive(empty + 8u * slot);
+    if (TEAMS && lane == 0) mbar_arrive(empty + 8u * slot);
     if (++slot == slots) {
       slot = 0;
       phase ^= 1u;
