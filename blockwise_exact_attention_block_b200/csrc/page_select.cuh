@@ -67,7 +67,8 @@ constexpr int kScoreThreads = 128;
 // products and is short by no more than that part of it.
 constexpr float kScoreError = 0x1.01p-15f;
 
-// Grid (page blocks, Hkv, B); a warp takes 16 pages, the M side of mma.m16n8k16,
+// Grid (page blocks, Hkv, B), striding over the pages that there are; a warp takes
+// 16 pages at a time, the M side of mma.m16n8k16,
 // with up to 8 query rows at a time on the N side and the 2 D columns (lo, then
 // hi) as K.  A lane reads its pages' bounds as whole 16-byte chunks qd + 4 j and
 // uses them as the K columns of two steps, with the query in the same order.
@@ -78,112 +79,116 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_
   const int b = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 31;
   const int gr = lane >> 2, qd = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int p0 = (blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5)) * 16;
-  if (p0 >= a.bt.max_pages) return;
-  // lengths, table and queries are loaded side by side; the lengths say afterwards what counts
-  const int raw = lane < 16 && p0 + lane < a.bt.max_pages
-                      ? a.bt.page_table[static_cast<long long>(b) * a.bt.max_pages + p0 + lane]
-                      : 0;
-  uint4 q0[J];
-#pragma unroll
-  for (int j = 0; j < J; ++j)
-    q0[j] = gr < a.rows ? *(reinterpret_cast<const uint4*>(select_row(a, b, h, gr, D)) + qd + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
-  const SeqLen s = seq_len_of(a.bt, b);
-  const int count = first_new_page(s, a.bt.page_shift);  // the others need no score
-  if (p0 >= count) return;
-  const bool bad = lane < 16 && p0 + lane < count && (raw < 0 || raw >= a.bt.n_pages);
-  if (bad) set_status(RA_ERR_DEVICE_BOUNDS);
-  const int mine = bad || p0 + lane >= count ? 0 : raw;  // a page without bounds is read as page 0 and not written
-  const int real = s.fresh * a.groups;                   // rows of real tokens come first
-  uint32_t lo[2][J][4], hi[2][J][4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {  // pages gr and gr + 8
-    const int page = __shfl_sync(0xffffffffu, mine, gr + 8 * i);
-    const uint4* src = reinterpret_cast<const uint4*>(a.bounds + (static_cast<long long>(page) * a.bt.Hkv + h) * 2 * D) + qd;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const uint4 x = src[4 * j], y = src[D / 8 + 4 * j];
-      lo[i][j][0] = x.x, lo[i][j][1] = x.y, lo[i][j][2] = x.z, lo[i][j][3] = x.w;
-      hi[i][j][0] = y.x, hi[i][j][1] = y.y, hi[i][j][2] = y.z, hi[i][j][3] = y.w;
-    }
-  }
-  uint32_t bmax = 0, qmax = 0;  // largest magnitudes, as pairs of bf16 bits
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int p0 = (blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5)) * 16; p0 < a.bt.max_pages;
+       p0 += gridDim.x * (kScoreThreads / 32) * 16) {
+    // lengths, table and queries are loaded side by side; the lengths say afterwards what counts
+    const int raw = lane < 16 && p0 + lane < a.bt.max_pages
+                        ? a.bt.page_table[static_cast<long long>(b) * a.bt.max_pages + p0 + lane]
+                        : 0;
+    uint4 q0[J];
 #pragma unroll
     for (int j = 0; j < J; ++j)
+      q0[j] = gr < a.rows ? *(reinterpret_cast<const uint4*>(select_row(a, b, h, gr, D)) + qd + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
+    const SeqLen s = seq_len_of(a.bt, b);
+    const int count = first_new_page(s, a.bt.page_shift);  // the others need no score
+    if (p0 >= count) return;
+    const bool bad = lane < 16 && p0 + lane < count && (raw < 0 || raw >= a.bt.n_pages);
+    if (bad) set_status(RA_ERR_DEVICE_BOUNDS);
+    const int mine = bad || p0 + lane >= count ? 0 : raw;  // a page without bounds is read as page 0 and not written
+    const int real = s.fresh * a.groups;                   // rows of real tokens come first
+    if (gr >= real)
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        // the smaller and the larger of the two, whatever the caller's order
-        const uint32_t x = lo[i][j][w], y = hi[i][j][w];
-        lo[i][j][w] = bf16x2_min(x, y);
-        hi[i][j][w] = bf16x2_max(x, y);
-      }
-  float best[2] = {-INFINITY, -INFINITY}, err[2] = {0.f, 0.f};
-  for (int r0 = 0; r0 < real; r0 += 8) {
-    if (r0 > 0)
+      for (int j = 0; j < J; ++j) q0[j] = make_uint4(0u, 0u, 0u, 0u);  // (padding may hold anything)
+    uint32_t lo[2][J][4], hi[2][J][4];
 #pragma unroll
-      for (int j = 0; j < J; ++j)
-        q0[j] = r0 + gr < real ? *(reinterpret_cast<const uint4*>(select_row(a, b, h, r0 + gr, D)) + qd + 4 * j)
-                               : make_uint4(0u, 0u, 0u, 0u);
-    float c[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};  // scores, and their terms' magnitudes
+    for (int i = 0; i < 2; ++i) {  // pages gr and gr + 8
+      const int page = __shfl_sync(0xffffffffu, mine, gr + 8 * i);
+      const uint4* src = reinterpret_cast<const uint4*>(a.bounds + (static_cast<long long>(page) * a.bt.Hkv + h) * 2 * D) + qd;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const uint32_t w[4] = {q0[j].x, q0[j].y, q0[j].z, q0[j].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) qmax = __vmaxu2(qmax, w[i] & 0x7fff7fffu);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const uint32_t al[4] = {lo[0][j][2 * t], lo[1][j][2 * t], lo[0][j][2 * t + 1], lo[1][j][2 * t + 1]};
-        const uint32_t ah[4] = {hi[0][j][2 * t], hi[1][j][2 * t], hi[0][j][2 * t + 1], hi[1][j][2 * t + 1]};
-        uint32_t aa[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          aa[i] = bf16x2_max(al[i] & 0x7fff7fffu, ah[i] & 0x7fff7fffu);
-          bmax = __vmaxu2(bmax, aa[i]);
-        }
-        pg_mma<kCacheBf16>(c, al, bf16x2_min(w[2 * t], 0u), bf16x2_min(w[2 * t + 1], 0u));
-        pg_mma<kCacheBf16>(c, ah, bf16x2_max(w[2 * t], 0u), bf16x2_max(w[2 * t + 1], 0u));
-        pg_mma<kCacheBf16>(m, aa, w[2 * t] & 0x7fff7fffu, w[2 * t + 1] & 0x7fff7fffu);
+      for (int j = 0; j < J; ++j) {
+        const uint4 x = src[4 * j], y = src[D / 8 + 4 * j];
+        lo[i][j][0] = x.x, lo[i][j][1] = x.y, lo[i][j][2] = x.z, lo[i][j][3] = x.w;
+        hi[i][j][0] = y.x, hi[i][j][1] = y.y, hi[i][j][2] = y.z, hi[i][j][3] = y.w;
       }
     }
-    // c[2 i + e], m[2 i + e]: page gr + 8 i, row r0 + 2 qd + e
+    uint32_t bmax = 0, qmax = 0;  // largest magnitudes, as pairs of bf16 bits
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (r0 + 2 * qd + e < real) {
-          best[i] = fmaxf(best[i], c[2 * i + e]);
-          // magnitudes that are not finite (an overflow) leave the pages to the exact sums
-          err[i] = m[2 * i + e] < 3e38f ? fmaxf(err[i], m[2 * i + e]) : INFINITY;
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          // the smaller and the larger of the two, whatever the caller's order
+          const uint32_t x = lo[i][j][w], y = hi[i][j][w];
+          lo[i][j][w] = bf16x2_min(x, y);
+          hi[i][j][w] = bf16x2_max(x, y);
         }
-  }
-  uint32_t big = max(max(bmax & 0xffffu, bmax >> 16), max(qmax & 0xffffu, qmax >> 16));
+    float best[2] = {-INFINITY, -INFINITY}, err[2] = {0.f, 0.f};
+    for (int r0 = 0; r0 < real; r0 += 8) {
+      if (r0 > 0)
 #pragma unroll
-  for (int x = 1; x < 32; x <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, x));
-  // Should the tensor core flush subnormal operands, products or sums: 256 terms
-  // of at most 2^-126 times the largest operand, or 2^-126.  Infinite and NaN
-  // operands leave the warp's pages to the exact sums.
-  const float floor_err = big >= 0x7f80u ? INFINITY : 0x1p-110f * fmaxf(__uint_as_float(big << 16), 1.f);
-  float* scores = reinterpret_cast<float*>(a.slots + (static_cast<long long>(b) * a.bt.Hkv + h) * a.stride);
-  float e = fmaxf(err[0], err[1]), all = -INFINITY;
+        for (int j = 0; j < J; ++j)
+          q0[j] = r0 + gr < real ? *(reinterpret_cast<const uint4*>(select_row(a, b, h, r0 + gr, D)) + qd + 4 * j)
+                                 : make_uint4(0u, 0u, 0u, 0u);
+      float c[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};  // scores, and their terms' magnitudes
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+      for (int j = 0; j < J; ++j) {
+        const uint32_t w[4] = {q0[j].x, q0[j].y, q0[j].z, q0[j].w};
 #pragma unroll
-    for (int x = 1; x < 4; x <<= 1) best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], x));
-    const int p = p0 + gr + 8 * i;
-    if (__shfl_sync(0xffffffffu, static_cast<int>(bad), gr + 8 * i) || p >= count) best[i] = -INFINITY;
-    if (qd == 0) scores[p] = best[i];  // (the stride is a multiple of 16)
-    all = fmaxf(all, best[i]);
-  }
+        for (int i = 0; i < 4; ++i) qmax = __vmaxu2(qmax, w[i] & 0x7fff7fffu);
 #pragma unroll
-  for (int x = 1; x < 32; x <<= 1) {
-    e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, x));
-    all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, x));
-  }
-  if (lane == 0) {
-    scores[a.stride + p0 / 16] = all;
-    scores[a.stride + a.stride / 16 + p0 / 16] = real > 0 ? fmaf(kScoreError, e, floor_err) : 0.f;
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t al[4] = {lo[0][j][2 * t], lo[1][j][2 * t], lo[0][j][2 * t + 1], lo[1][j][2 * t + 1]};
+          const uint32_t ah[4] = {hi[0][j][2 * t], hi[1][j][2 * t], hi[0][j][2 * t + 1], hi[1][j][2 * t + 1]};
+          uint32_t aa[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            aa[i] = bf16x2_max(al[i] & 0x7fff7fffu, ah[i] & 0x7fff7fffu);
+            bmax = __vmaxu2(bmax, aa[i]);
+          }
+          pg_mma<kCacheBf16>(c, al, bf16x2_min(w[2 * t], 0u), bf16x2_min(w[2 * t + 1], 0u));
+          pg_mma<kCacheBf16>(c, ah, bf16x2_max(w[2 * t], 0u), bf16x2_max(w[2 * t + 1], 0u));
+          pg_mma<kCacheBf16>(m, aa, w[2 * t] & 0x7fff7fffu, w[2 * t + 1] & 0x7fff7fffu);
+        }
+      }
+      // c[2 i + e], m[2 i + e]: page gr + 8 i, row r0 + 2 qd + e
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (r0 + 2 * qd + e < real) {
+            best[i] = fmaxf(best[i], c[2 * i + e]);
+            // magnitudes that are not finite (an overflow) leave the pages to the exact sums
+            err[i] = m[2 * i + e] < 3e38f ? fmaxf(err[i], m[2 * i + e]) : INFINITY;
+          }
+    }
+    uint32_t big = max(max(bmax & 0xffffu, bmax >> 16), max(qmax & 0xffffu, qmax >> 16));
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, x));
+    // Should the tensor core flush subnormal operands, products or sums: 256 terms
+    // of at most 2^-126 times the largest operand, or 2^-126.  Infinite and NaN
+    // operands leave the warp's pages to the exact sums.
+    const float floor_err = big >= 0x7f80u ? INFINITY : 0x1p-110f * fmaxf(__uint_as_float(big << 16), 1.f);
+    float* scores = reinterpret_cast<float*>(a.slots + (static_cast<long long>(b) * a.bt.Hkv + h) * a.stride);
+    float e = fmaxf(err[0], err[1]), all = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int x = 1; x < 4; x <<= 1) best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], x));
+      const int p = p0 + gr + 8 * i;
+      if (__shfl_sync(0xffffffffu, static_cast<int>(bad), gr + 8 * i) || p >= count) best[i] = -INFINITY;
+      if (qd == 0) scores[p] = best[i];  // (the stride is a multiple of 16)
+      all = fmaxf(all, best[i]);
+    }
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, x));
+      all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, x));
+    }
+    if (lane == 0) {
+      scores[a.stride + p0 / 16] = all;
+      scores[a.stride + a.stride / 16 + p0 / 16] = real > 0 ? fmaf(kScoreError, e, floor_err) : 0.f;
+    }
   }
 }
 
@@ -363,16 +368,16 @@ __device__ __forceinline__ Key kth_largest(SelectShared& sh, Each&& each, int wa
 
 // One CTA per (sequence, KV head).  The new tokens' pages are in; `want` of the n
 // scored pages are chosen.
-//  - Candidates: the want-th largest of the maxima of 16 pages each has at least
-//    `want` scores at or above it, so no page more than two errors below it can
-//    win; the rest are listed in shared memory.
+//  - Candidates, of many pages: the want-th largest of the maxima of 16 pages each
+//    has at least `want` scores at or above it, so no page more than two errors
+//    below it can win; the rest are listed in shared memory.
 //  - With T the want-th largest fp32 score and err the largest error of any, a page
 //    above T + 2 err is in and one below T - 2 err is out (the want-th largest exact
 //    score lies within err of T); those between, usually a handful, are ranked by
 //    their exact keys, ties to the lower page.
 //  - The chosen indices come out in page order.
-// Where the candidates are too many for the list, the same passes read all scores
-// from memory; where many are close (equal or infinite scores), every page gets
+// Where the pages are few or the candidates too many for the list, the same passes
+// read all scores from memory; where many are close (equal or infinite scores), every page gets
 // its exact key and the search runs on those.
 template <int D>
 __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_constant__ SelectArgs a) {
@@ -409,9 +414,9 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
   bool many = !(err < 3e38f);     // infinite or NaN scores
   int above, N = n;               // items of the search: the list's, or all pages
   bool listed = false;
-  if (!many && (want <= groups || n <= kSelList)) {
-    uint32_t least = 0;  // key of the lowest score that can win
-    if (want <= groups) {
+  if (!many && want <= groups && n > kSelList) {
+    uint32_t least;  // key of the lowest score that can win
+    {
       const uint32_t k = kth_largest<uint32_t>(
           sh,
           [&](auto&& fn) {

@@ -169,7 +169,10 @@ int page_span(int T, int page_size) {
 template <int D>
 ra_status launch_select_d(const SelectArgs& a, cudaStream_t st) {
   const int per = 16 * (kScoreThreads / 32);  // pages of a block
-  const dim3 grid(static_cast<unsigned>((a.bt.max_pages + per - 1) / per), a.bt.Hkv, a.bt.B);
+  // blocks for the table's width, up to 32 an SM over all pairs: the sequences may be much shorter
+  const long long pairs = static_cast<long long>(a.bt.B) * a.bt.Hkv;
+  const long long need = (a.bt.max_pages + per - 1) / per, most = (32LL * sm_count() + pairs - 1) / pairs;
+  const dim3 grid(static_cast<unsigned>(need < most ? need : most), a.bt.Hkv, a.bt.B);
   page_score_kernel<D><<<grid, kScoreThreads, 0, st>>>(a);
   const ra_status s = cuda_status(cudaGetLastError());
   if (s != RA_OK) return s;

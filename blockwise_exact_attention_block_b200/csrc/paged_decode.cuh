@@ -228,16 +228,17 @@ __device__ __forceinline__ void split_pair(float x, float y, bool three, uint32_
   }
 }
 
-// Tiles of one (sequence, KV head) pair.
-__device__ __forceinline__ int pg_tiles(const PagedArgs& a, int len) {
-  if (a.selected == nullptr) return (len + kPgKeys - 1) / kPgKeys;
-  const int pages = (len + (1 << a.bt.page_shift) - 1) >> a.bt.page_shift;
+// Tiles of one (sequence, KV head) pair; none where no row is real.
+__device__ __forceinline__ int pg_tiles(const PagedArgs& a, const SeqLen& s) {
+  if (s.fresh == 0) return 0;
+  if (a.selected == nullptr) return (s.len + kPgKeys - 1) / kPgKeys;
+  const int pages = (s.len + (1 << a.bt.page_shift) - 1) >> a.bt.page_shift;
   return ((min(a.n_sel, pages) << a.bt.page_shift) + kPgKeys - 1) / kPgKeys;
 }
 
 // Units of the line that a sequence takes: its pairs' tiles and costs.
-__device__ __forceinline__ long long pg_units(const PagedArgs& a, int len) {
-  const int n = pg_tiles(a, len);
+__device__ __forceinline__ long long pg_units(const PagedArgs& a, const SeqLen& s) {
+  const int n = pg_tiles(a, s);
   return n > 0 ? static_cast<long long>(n + kPgPairCost) * a.bt.Hkv : 0;
 }
 
@@ -264,9 +265,9 @@ __device__ __forceinline__ long long quotient(long long x, long long y) {
 // The walker warp: lane t < teams walks the run of team t.  In every round the
 // lanes whose queue has room post one tile.  Page numbers are loaded when a
 // tile is reached and used in the round that posts it, so their latency
-// overlaps the rounds between.  len0: the length of sequence `lane`.
+// overlaps the rounds between.  own: the units of sequence `lane`.
 template <int D, int ET, int NB, bool TEAMS>
-__device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volatile int* abort_flag, int len0) {
+__device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volatile int* abort_flag, long long own) {
   using SL = PgSmem<D, ET, NB, TEAMS>;
   const int lane = threadIdx.x & 31;
   const int teams = SL::kWarps / a.R;
@@ -276,11 +277,8 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
   const int ps = 1 << a.bt.page_shift;
 
   // the line and this lane's run [f0, f0 + n) of it; lane i holds the units of sequence i of each 32
-  long long total = 0, own = 0;
-  for (int i = lane; i < a.bt.B; i += 32) {
-    own = pg_units(a, i == lane ? len0 : seq_len_of(a.bt, i).len);
-    total += own;
-  }
+  long long total = own;
+  for (int i = lane + 32; i < a.bt.B; i += 32) total += pg_units(a, seq_len_of(a.bt, i));
 #pragma unroll
   for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const long long U = static_cast<long long>(gridDim.x) * teams;
@@ -296,25 +294,30 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
     long long before = 0;
     bool found = false;
     for (int b0 = 0; b0 < a.bt.B; b0 += 32) {
-      if (a.bt.B > 32) own = b0 + lane < a.bt.B ? pg_units(a, seq_len_of(a.bt, b0 + lane).len) : 0;
-      long long upto = b0 + lane < a.bt.B ? own : 0;
-      const long long mine = upto;
+      if (b0 > 0) own = b0 + lane < a.bt.B ? pg_units(a, seq_len_of(a.bt, b0 + lane)) : 0;
+      long long upto = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += x;
       }
-      const int m = min(32, a.bt.B - b0);
-      for (int i = 0; i < m; ++i) {
-        const long long e = before + __shfl_sync(0xffffffffu, upto, i);
-        const long long x = e - __shfl_sync(0xffffffffu, mine, i);
-        if (work && !found && f0 < e) {
+      const long long end = before + __shfl_sync(0xffffffffu, upto, 31);
+      const bool here = work && !found && f0 < end;
+      if (__any_sync(0xffffffffu, here)) {  // the first sequence that ends behind f0
+        int i = 0;
+#pragma unroll
+        for (int step = 16; step; step >>= 1) {
+          const long long x = before + __shfl_sync(0xffffffffu, upto, i + step - 1);
+          if (here && f0 >= x) i += step;
+        }
+        const long long x = before + __shfl_sync(0xffffffffu, upto - own, i);
+        if (here) {
           found = true;
           b = b0 + i;
           start = x;
         }
       }
-      before += __shfl_sync(0xffffffffu, upto, 31);
+      before = end;
     }
   }
   SeqLen s = {0, 0};
@@ -322,7 +325,7 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
   int pair = 0;  // the pair's first unit, from f0 (negative where an earlier team began it)
   if (work) {
     s = seq_len_of(a.bt, b);
-    nt = pg_tiles(a, s.len);
+    nt = pg_tiles(a, s);
     const long long rel = f0 - start;
     h = static_cast<int>(quotient(rel, nt + kPgPairCost));
     pair = static_cast<int>(static_cast<long long>(h) * (nt + kPgPairCost) - rel);
@@ -341,7 +344,7 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
           do {
             ++b;
             s = b < a.bt.B ? seq_len_of(a.bt, b) : SeqLen{0, 0};
-            nt = pg_tiles(a, s.len);
+            nt = pg_tiles(a, s);
           } while (b < a.bt.B && nt == 0);
           if (b >= a.bt.B) work = false;
         }
@@ -467,8 +470,8 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
 
   // the combine kernel may be brought onto the SMs; it waits for this grid's end itself
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int len0 = 0;  // the walker's first lengths, on their way while the barriers are set up
-  if (warp == SL::kWarps && lane < a.bt.B) len0 = seq_len_of(a.bt, lane).len;
+  long long own = 0;  // the walker's first lengths, on their way while the barriers are set up
+  if (warp == SL::kWarps && lane < a.bt.B) own = pg_units(a, seq_len_of(a.bt, lane));
   if (tid == 32 * SL::kWarps) *abort_flag = grid_timed_out() ? 1 : 0;
   for (int i = tid; i < teams * slots; i += SL::kThreads) {
     mbar_init(sb + SL::kFull + 8u * i, 32 * a.R);  // every thread of the team
@@ -482,13 +485,13 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
   __syncthreads();
   if (*abort_flag) return;
   if (warp == SL::kWarps) {
-    pg_walk<D, ET, NB, TEAMS>(a, smem, abort_flag, len0);
+    pg_walk<D, ET, NB, TEAMS>(a, smem, abort_flag, own);
     return;
   }
 
-  // sequences without a tile: their rows are empty
+  // sequences without a tile (empty or idle): their rows are empty
   for (int b = blockIdx.x * SL::kWarps + warp; b < a.bt.B; b += gridDim.x * SL::kWarps) {
-    if (pg_tiles(a, seq_len_of(a.bt, b).len) > 0) continue;
+    if (pg_tiles(a, seq_len_of(a.bt, b)) > 0) continue;
     const long long q0 = static_cast<long long>(b) * a.bt.T * a.Hq, n = static_cast<long long>(a.bt.T) * a.Hq;
     for (long long i = lane; i < n * (D / 2); i += 32)
       pg_store2(a, q0 + i / (D / 2), D, 2 * static_cast<int>(i % (D / 2)), 0.f, 0.f);

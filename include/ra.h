@@ -315,7 +315,8 @@ int ra_decode_splits(int B, int Tq, int Skv, int Hq, int Hkv, int D, int n_split
  *  k_pages, v_pages  device, `dtype` (RA_BF16, RA_I8 or RA_E4M3), [n_pages, Hkv,
  *             page_size, D]: the rows of one KV head of one page are adjacent.
  *  k_scales, v_scales  device fp32 [n_pages, Hkv, page_size]: one scale for
- *             each row of an 8-bit cache (value = code * scale); NULL for RA_BF16.
+ *             each row of an 8-bit cache (value = code * scale, scale >= 0; e4m3
+ *             codes other than the NaNs); NULL for RA_BF16.
  *  key_bounds  device bf16 [n_pages, Hkv, 2, D]: for each column the smallest
  *             and the largest key of the page.  NULL where a call does not use it.
  *  dtype, n_pages, page_size, Hkv, D   page_size in {16, 32, 64, 128}; D in

@@ -87,6 +87,65 @@ def test_subnormal_huge_and_zero_bounds(cuda_lib):
     assert ra.ra_get_device_status() == ra.RA_OK
 
 
+def test_padding_rows_and_wide_tables(cuda_lib):
+    """Query rows that are not real hold NaN; the table is far wider than the lengths."""
+    ra = cuda_lib
+    seq, new = [900, 333, 50], [2, 1, 3]
+    q, bounds, table = draw(3, 3, 8, 2, 128, 16, seq, 7)
+    want = P.select(f64(q), f64(bounds), 16, table.tolist(), seq, new, 9)
+    for b, n in enumerate(new):
+        q[b, n:] = float("nan")
+    wide = torch.full((3, 60000), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    got = ra.ra_page_select(q.cuda(), bounds.cuda(), wide.cuda(), torch.tensor(seq, dtype=torch.int32).cuda(), 9, 16,
+                            new_lens=torch.tensor(new, dtype=torch.int32).cuda())
+    assert np.array_equal(got.cpu().numpy(), want)
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
+def test_scores_closer_than_fp32_can_tell(cuda_lib):
+    """Pages whose scores differ by one unit of 2^-30 beside terms of 2^10: the fp32
+    pass cannot order them, the exact sums do.  More of them than are compared in
+    shared memory, too."""
+    ra = cuda_lib
+    D, ps = 64, 16
+    gen = torch.Generator().manual_seed(9)
+    for n in (100, 3000):
+        b = torch.zeros((n, 1, D), dtype=torch.bfloat16)
+        b[..., :8] = 1024.0
+        b[..., 9] = torch.randint(0, 16, (n, 1), generator=gen).float().to(torch.bfloat16) * 2.0 ** -30
+        b[..., 10] = torch.randint(0, 16, (n, 1), generator=gen).float().to(torch.bfloat16) * 2.0 ** -26
+        bounds = torch.stack((b, b), 2).contiguous()
+        q = torch.ones((1, 1, 2, D), dtype=torch.bfloat16)
+        table = torch.randperm(n, generator=gen).to(torch.int32)[None].contiguous()
+        for n_sel in (2, 37):
+            got = ra.ra_page_select(q.cuda(), bounds.cuda(), table.cuda(), torch.tensor([n * ps], dtype=torch.int32).cuda(),
+                                    n_sel, ps)
+            want = P.select(f64(q), f64(bounds), ps, table.tolist(), [n * ps], [1], n_sel)
+            assert np.array_equal(got.cpu().numpy(), want), (n, n_sel)
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
+def test_infinite_keys_and_queries(cuda_lib):
+    """An infinite bound counts as 2^128; a row whose sum is NaN does not count."""
+    ra = cuda_lib
+    q, bounds, table = draw(1, 2, 4, 1, 64, 16, [16 * 40], 3)
+    bounds[5, 0, 1, 7] = float("inf")
+    bounds[9, 0, 0, 3] = -float("inf")
+    want = P.select(f64(q), f64(bounds), 16, table.tolist(), [16 * 40], [2], 12)
+    lens = torch.tensor([16 * 40], dtype=torch.int32).cuda()
+    got = ra.ra_page_select(q.cuda(), bounds.cuda(), table.cuda(), lens, 12, 16)
+    assert np.array_equal(got.cpu().numpy(), want)
+    q2 = q.clone()
+    q2[0, 1] = float("nan")  # the second token's rows count for nothing
+    want = P.select(f64(q[:, :1]), f64(bounds), 16, table.tolist(), [16 * 40], [1], 12)
+    lens.fill_(16 * 40)
+    got = ra.ra_page_select(q2.cuda(), bounds.cuda(), table.cuda(), lens, 12, 16)
+    last = (16 * 40 - 2) // 16
+    assert last == 39 and np.array_equal(got.cpu().numpy(), want)
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
 def test_bad_pages_are_recorded(cuda_lib):
     ra = cuda_lib
     q, bounds, table = draw(2, 1, 4, 2, 64, 16, [300, 200], 0)

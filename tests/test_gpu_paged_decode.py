@@ -298,6 +298,49 @@ def test_graph_stream_and_workspace(cuda_lib):
     assert ra.ra_get_device_status() == ra.RA_OK
 
 
+def test_a_large_batch_with_idle_sequences(cuda_lib):
+    """More sequences than the walker's warp, several chunks of empty and idle ones between."""
+    ra = cuda_lib
+    seq = [(7 * b) % 53 if b % 3 else 0 for b in range(300)]
+    new = [min(1, n) if b % 5 else 0 for b, n in enumerate(seq)]
+    seq[137], new[137], seq[299], new[299] = 2500, 1, 41, 1
+    c = Case("int8", 300, 1, 4, 2, 64, 16, seq, new, seed=5)
+    got = ra.ra_paged_decode_attention(*c.args, out_dtype=torch.bfloat16, **c.kw)
+    c.check(got, True)
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
+def test_a_table_much_wider_than_the_sequences(cuda_lib):
+    ra = cuda_lib
+    c = Case("e4m3", 2, 1, 8, 2, 128, 16, [100, 33], seed=5)
+    wide = torch.full((2, 70000), -1, dtype=torch.int32)
+    wide[:, :c.table.shape[1]] = c.table
+    q, kp, vp, _, lens = c.args
+    c.check(ra.ra_paged_decode_attention(q, kp, vp, wide.cuda(), lens, out_dtype=torch.bfloat16, **c.kw), True)
+    k, _ = ra.ra_cache_read(kp, vp, wide.cuda(), lens, 40, first=80, k_scales=c.scales["k"], v_scales=c.scales["v"])
+    assert not k[0, 20:].any() and not k[1].any() and k[0, :20].any()
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
+def test_two_streams_at_once(cuda_lib):
+    """Calls that overlap, each with a workspace of its own."""
+    ra = cuda_lib
+    cases = [Case("bf16", 3, 1, 8, 2, 128, 16, [3000, 1000, 2500], seed=1),
+             Case("int8", 3, 4, 8, 2, 128, 16, [2000, 2200, 300], seed=2)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    ws = [torch.empty(ra.ra_paged_decode_workspace(3, c.q.shape[1], 8, 2, 128), dtype=torch.uint8, device="cuda") for c in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for c, st, w in zip(cases, streams, ws):
+            with torch.cuda.stream(st):
+                got.append(ra.ra_paged_decode_attention(*c.args, workspace=w, out_dtype=torch.bfloat16, **c.kw))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        cases[i % 2].check(g, True)
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
 def test_a_serving_run(cuda_lib):
     """Prompt, appended in chunks; then decoded token by token: the paged calls
     against the dense decode over the same (bf16) cache, and ra_ring_attention over
