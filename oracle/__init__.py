@@ -32,10 +32,12 @@ Modules:
   and the pages' merge rule, fp64.  Shares no code with ``attention``.
 * ``backward``   - gradients (dq, dk, dv): the definition over whole rows and
   the same gradient as sums over block pairs rebuilt from the full-row lse.
+* ``paged``      - the paged key-value cache: append with its 8-bit rounding,
+  read-back, decode over pages, page selection by key bounds.
 
 Every function here is pinned by ``tests/test_oracle.py`` against brute force,
 closed forms, a library routine or an invariant the pages fix.  The timing
 columns of the pages (7.6 ms / 3.5 ms on four A10s) are "parity unpinned": they
 need hardware and a model shape the pages do not give.
 """
-from . import attention, backward, blockwise  # noqa: F401
+from . import attention, backward, blockwise, paged  # noqa: F401
