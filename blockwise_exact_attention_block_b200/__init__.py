@@ -17,7 +17,8 @@ torch.distributed point-to-point messages.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -34,6 +35,19 @@ if not os.path.exists(LIB_PATH):
         f"{' --debug-bounds' if DEBUG_BOUNDS else ''}`")
 
 _lib = ctypes.CDLL(LIB_PATH)
+
+
+def _load_paged():
+    """The extension module that marshals the paged cache's calls."""
+    path = os.path.join(_PKG, "_paged.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with `python blockwise_exact_attention_block_b200/build.py`")
+    name = __name__ + "._paged"
+    loader = importlib.machinery.ExtensionFileLoader(name, path)
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader(name, loader))
+    loader.exec_module(mod)
+    return mod
+
 
 RA_OK, RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_WORKSPACE = 0, 1, 2, 3
 RA_ERR_CUDA, RA_ERR_TIMEOUT, RA_ERR_DEVICE_BOUNDS = 4, 5, 6
@@ -445,59 +459,18 @@ def ra_decode_attention(q, k, v, causal: bool = True, n_splits: int = 0, out=Non
 # [n_pages, Hkv, 2, D]; page_table int32 [B, max_pages], seq_lens and new_lens
 # int32 [B] on the device: see ra_paged_cache in include/ra.h.
 
-_CACHE_DTYPES = {torch.bfloat16: RA_BF16, torch.int8: RA_I8, torch.float8_e4m3fn: RA_E4M3}
+# The calls are marshalled by the extension module _paged (csrc/paged_binding.cpp):
+# a decoding step makes several for every token, and checking a dozen tensors in
+# Python took longer than the kernels.
+
+_paged = _load_paged()
+_fn = {name: ctypes.cast(getattr(_lib, name), _vp).value
+       for name in ("ra_cache_append", "ra_cache_read", "ra_paged_decode_attention", "ra_paged_decode_workspace",
+                    "ra_page_select", "ra_page_select_workspace")}
 
 
-def _expect(t: torch.Tensor | None, name: str, dtype, shape, device: int) -> int | None:
-    """The address of t, checked: contiguous, on CUDA device `device`, of this dtype and shape."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on cuda:{device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _paged(k_pages, v_pages, k_scales, v_scales, key_bounds, page_table, seq_lens, new_lens) -> ra_paged_cache:
-    """The C argument of a cache and its batch (shapes and devices checked)."""
-    if not k_pages.is_cuda:
-        raise ValueError("tensors must be contiguous CUDA tensors")
-    dev, dtype, shape, tab = k_pages.get_device(), k_pages.dtype, k_pages.shape, page_table.shape
-    if len(shape) != 4 or dtype not in _CACHE_DTYPES:
-        raise ValueError("k_pages must be [n_pages, Hkv, page_size, D] in bfloat16, int8 or float8_e4m3fn")
-    if len(tab) != 2:
-        raise ValueError("page_table must be [B, max_pages]")
-    n_pages, Hkv, page_size, D = shape
-    B, max_pages = tab
-    code = _CACHE_DTYPES[dtype]
-    if (code == RA_BF16) != (k_scales is None) or (code == RA_BF16) != (v_scales is None):
-        raise ValueError("an 8-bit cache has k_scales and v_scales, a bfloat16 one has none")
-    f32, i32 = torch.float32, torch.int32
-    rows, lens = (n_pages, Hkv, page_size), (B,)
-    return ra_paged_cache(
-        _expect(k_pages, "k_pages", dtype, shape, dev), _expect(v_pages, "v_pages", dtype, shape, dev),
-        _expect(k_scales, "k_scales", f32, rows, dev), _expect(v_scales, "v_scales", f32, rows, dev),
-        _expect(key_bounds, "key_bounds", torch.bfloat16, (n_pages, Hkv, 2, D), dev), code, n_pages, page_size, Hkv, D,
-        _expect(page_table, "page_table", i32, tab, dev), B, max_pages,
-        _expect(seq_lens, "seq_lens", i32, lens, dev), _expect(new_lens, "new_lens", i32, lens, dev))
-
-
-# the current stream's handle of a device; torch.cuda.current_stream builds a Stream object to say the same
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
-def _call_on(dev: int, stream, fn, what: str, *args) -> None:
-    """fn(*args, stream) with CUDA device `dev` current, on the given stream or on
-    dev's current one (not another device's)."""
-    handle = _raw_stream(dev) if stream is None else _stream(stream)
-    if torch.cuda.current_device() != dev:
-        with torch.cuda.device(dev):
-            status = fn(*args, handle)
-    else:
-        status = fn(*args, handle)
-    if status != RA_OK:
-        raise RAError(status, what)
+def _handle(stream) -> int | None:
+    return None if stream is None else _stream(stream)
 
 
 def ra_cache_append(k, v, k_pages, v_pages, page_table, seq_lens, new_lens=None, k_scales=None, v_scales=None,
@@ -506,13 +479,10 @@ def ra_cache_append(k, v, k_pages, v_pages, page_table, seq_lens, new_lens=None,
     scales of an 8-bit cache and, if given, the pages' key bounds.  seq_lens
     counts the new tokens in; row i < new_lens[b] is the token at position
     seq_lens[b] - new_lens[b] + i (None: min(T, seq_lens[b]) of them)."""
-    c = _paged(k_pages, v_pages, k_scales, v_scales, key_bounds, page_table, seq_lens, new_lens)
-    if k.dim() != 4:
-        raise ValueError("k must be [B, T, Hkv, D]")
-    T = k.shape[1]
-    shape, dev = (c.B, T, c.Hkv, c.D), k_pages.get_device()
-    _call_on(dev, stream, _lib.ra_cache_append, "ra_cache_append", ctypes.byref(c),
-             _expect(k, "k", k.dtype, shape, dev), _expect(v, "v", k.dtype, shape, dev), _dtype_code(k.dtype), T)
+    status = _paged.append(_fn["ra_cache_append"], k, v, k_pages, v_pages, page_table, seq_lens, new_lens, k_scales,
+                           v_scales, key_bounds, _handle(stream))
+    if status != RA_OK:
+        raise RAError(status, "ra_cache_append")
 
 
 def ra_cache_read(k_pages, v_pages, page_table, seq_lens, T: int, first: int = 0, k_scales=None, v_scales=None,
@@ -520,19 +490,13 @@ def ra_cache_read(k_pages, v_pages, page_table, seq_lens, T: int, first: int = 0
     """Tokens first .. first + T - 1 of every sequence as dense (k, v)
     [B, T, Hkv, D], zero at and behind seq_lens[b]; out_dtype bfloat16 (default)
     or float32."""
-    c = _paged(k_pages, v_pages, k_scales, v_scales, None, page_table, seq_lens, None)
-    shape, dev = (c.B, T, c.Hkv, c.D), k_pages.get_device()
-    odt = out_dtype or (k.dtype if k is not None else v.dtype if v is not None else torch.bfloat16)
-    if k is None:
-        k = k_pages.new_empty(shape, dtype=odt)
-    if v is None:
-        v = k_pages.new_empty(shape, dtype=odt)
-    _call_on(dev, stream, _lib.ra_cache_read, "ra_cache_read", ctypes.byref(c), first, T,
-             _expect(k, "k", odt, shape, dev), _expect(v, "v", odt, shape, dev), _dtype_code(odt))
+    status, k, v = _paged.read(_fn["ra_cache_read"], k_pages, v_pages, page_table, seq_lens, T, first, k_scales, v_scales,
+                               k, v, out_dtype, _handle(stream))
+    if status != RA_OK:
+        raise RAError(status, "ra_cache_read")
     return k, v
 
 
-@functools.lru_cache(maxsize=None)
 def ra_paged_decode_workspace(B, Tq, Hq, Hkv, D) -> int:
     n = _lib.ra_paged_decode_workspace(B, Tq, Hq, Hkv, D)
     if n == ctypes.c_size_t(-1).value:
@@ -548,32 +512,14 @@ def ra_paged_decode_attention(q, k_pages, v_pages, page_table, seq_lens, new_len
     gives them).  Row i < new_lens[b] is the token at position seq_lens[b] -
     new_lens[b] + i (None: min(Tq, seq_lens[b]) real rows).  Returns
     (out [B, Tq, Hq, D] in out_dtype, default float32; lse [B, Tq, Hq] float32)."""
-    c = _paged(k_pages, v_pages, k_scales, v_scales, None, page_table, seq_lens, new_lens)
-    if q.dim() != 4:
-        raise ValueError("q must be [B, Tq, Hq, D]")
-    _, Tq, Hq, _ = q.shape
-    shape, dev = (c.B, Tq, Hq, c.D), k_pages.get_device()
-    odt = out_dtype or (out.dtype if out is not None else torch.float32)
-    if out is None:
-        out = q.new_empty(shape, dtype=odt)
-    if lse is None:
-        lse = q.new_empty(shape[:3], dtype=torch.float32)
-    n_sel = 0
-    if selected is not None:
-        if selected.dim() != 3:
-            raise ValueError("selected must be [B, Hkv, n_sel]")
-        n_sel = selected.shape[2]
-    if workspace is None:
-        workspace = k_pages.new_empty(ra_paged_decode_workspace(c.B, Tq, Hq, c.Hkv, c.D), dtype=torch.uint8)
-    _call_on(dev, stream, _lib.ra_paged_decode_attention, "ra_paged_decode_attention", _expect(q, "q", q.dtype, shape, dev),
-             _dtype_code(q.dtype), ctypes.byref(c), Tq, Hq, int(bool(causal)),
-             _expect(selected, "selected", torch.int32, (c.B, c.Hkv, n_sel), dev), n_sel,
-             _expect(out, "out", odt, shape, dev), _dtype_code(odt), _expect(lse, "lse", torch.float32, shape[:3], dev),
-             _ptr(workspace), workspace.numel() * workspace.element_size())
+    status, out, lse = _paged.decode(_fn["ra_paged_decode_attention"], _fn["ra_paged_decode_workspace"], q, k_pages,
+                                     v_pages, page_table, seq_lens, new_lens, k_scales, v_scales, causal, selected, out,
+                                     lse, out_dtype, workspace, _handle(stream))
+    if status != RA_OK:
+        raise RAError(status, "ra_paged_decode_attention")
     return out, lse
 
 
-@functools.lru_cache(maxsize=None)
 def ra_page_select_workspace(B, Hkv, max_pages) -> int:
     n = _lib.ra_page_select_workspace(B, Hkv, max_pages)
     if n == ctypes.c_size_t(-1).value:
@@ -587,24 +533,8 @@ def ra_page_select(q, key_bounds, page_table, seq_lens, n_sel: int, page_size: i
     queries q [B, Tq, Hq, D] (bf16) by the bound that key_bounds
     [n_pages, Hkv, 2, D] puts on a page's scores: int32 [B, Hkv, n_sel],
     ascending, -1 behind.  The new tokens' own pages are always among them."""
-    if not key_bounds.is_cuda:
-        raise ValueError("tensors must be contiguous CUDA tensors")
-    if q.dim() != 4 or key_bounds.dim() != 4 or page_table.dim() != 2:
-        raise ValueError("q must be [B, Tq, Hq, D], key_bounds [n_pages, Hkv, 2, D], page_table [B, max_pages]")
-    n_pages, Hkv, _, D = key_bounds.shape
-    B, max_pages = page_table.shape
-    _, Tq, Hq, _ = q.shape
-    i32, dev = torch.int32, key_bounds.get_device()
-    c = ra_paged_cache(None, None, None, None,
-                       _expect(key_bounds, "key_bounds", torch.bfloat16, (n_pages, Hkv, 2, D), dev), RA_BF16, n_pages,
-                       page_size, Hkv, D, _expect(page_table, "page_table", i32, page_table.shape, dev), B, max_pages,
-                       _expect(seq_lens, "seq_lens", i32, (B,), dev), _expect(new_lens, "new_lens", i32, (B,), dev))
-    if selected is None:
-        selected = key_bounds.new_empty((B, Hkv, max(n_sel, 0)), dtype=i32)
-    if workspace is None:
-        workspace = key_bounds.new_empty(ra_page_select_workspace(B, Hkv, max_pages), dtype=torch.uint8)
-    _call_on(dev, stream, _lib.ra_page_select, "ra_page_select", _expect(q, "q", q.dtype, (B, Tq, Hq, D), dev),
-             _dtype_code(q.dtype), ctypes.byref(c), Tq, Hq, n_sel,
-             _expect(selected, "selected", i32, (B, Hkv, n_sel), dev), _ptr(workspace),
-             workspace.numel() * workspace.element_size())
+    status, selected = _paged.select(_fn["ra_page_select"], _fn["ra_page_select_workspace"], q, key_bounds, page_table,
+                                     seq_lens, n_sel, page_size, new_lens, selected, workspace, _handle(stream))
+    if status != RA_OK:
+        raise RAError(status, "ra_page_select")
     return selected

@@ -6,6 +6,8 @@
 
 csrc/api.cu is the main translation unit (it includes every kernel);
 csrc/noalloc.cu adds the entry point whose scratch is a fixed device array.
+csrc/paged_binding.cpp is the CPython extension _paged that marshals the paged
+cache's calls (compiled with the C++ compiler against torch's headers).
 --debug-bounds builds the checked variant libra_b200_debug.so instead
 (-DRA_DEBUG_BOUNDS: every run-time-indexed global access is checked; the
 binding loads it when RA_DEBUG_BOUNDS=1 is set in the environment).
@@ -22,6 +24,8 @@ ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", "api.cu"), os.path.join(PKG, "csrc", "noalloc.cu")]
 OUT = os.path.join(PKG, "libra_b200.so")
 OUT_DEBUG = os.path.join(PKG, "libra_b200_debug.so")
+BINDING_SRC = os.path.join(PKG, "csrc", "paged_binding.cpp")
+BINDING = os.path.join(PKG, "_paged.so")
 
 
 def nvcc_path() -> str:
@@ -44,7 +48,33 @@ def up_to_date(out: str = OUT) -> bool:
     return all(os.path.getmtime(s) <= t for s in sources())
 
 
+def build_binding(force: bool = False) -> str:
+    """The extension module of the paged cache's calls (host code only)."""
+    srcs = [BINDING_SRC, os.path.join(ROOT, "include", "ra.h")]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(s) <= os.path.getmtime(BINDING) for s in srcs):
+        return BINDING
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    inc = [os.path.join(ROOT, "include"), os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
+           sysconfig.get_paths()["include"]]
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{d}" for d in inc[:1]], *[f"-isystem{d}" for d in inc[1:]], BINDING_SRC, "-o", BINDING + ".tmp",
+           "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("c++ failed:\n" + res.stdout + res.stderr)
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
+
+
 def build(force: bool = False, ptxas_verbose: bool = False, debug_bounds: bool = False) -> str:
+    if not debug_bounds:
+        build_binding(force)
     out = OUT_DEBUG if debug_bounds else OUT
     if not force and up_to_date(out):
         return out

@@ -341,6 +341,71 @@ def test_two_streams_at_once(cuda_lib):
     assert ra.ra_get_device_status() == ra.RA_OK
 
 
+def test_the_binding_refuses(cuda_lib):
+    """Tensors of another type, shape, layout or device; outputs that do not fit; things that are no tensors."""
+    ra = cuda_lib
+    c = Case("int8", 2, 1, 4, 2, 64, 16, [40, 20], seed=1)
+    q, kp, vp, table, lens = c.args
+    ks, vs = c.scales["k"], c.scales["v"]
+
+    def call(**kw):
+        a = dict(q=q, k_pages=kp, v_pages=vp, page_table=table, seq_lens=lens, k_scales=ks, v_scales=vs)
+        a.update(kw)
+        return ra.ra_paged_decode_attention(**a)
+
+    call()
+    for bad in (dict(seq_lens=lens.long()), dict(seq_lens=lens.cpu()), dict(seq_lens=lens[:1]), dict(page_table=table.t()),
+                dict(page_table=table[:, ::2]), dict(page_table=table[0]), dict(new_lens=lens.float()),
+                dict(v_pages=vp.view(torch.uint8)), dict(v_pages=vp[:1]), dict(k_pages=kp[0]), dict(k_pages=kp.cpu()),
+                dict(k_scales=None), dict(v_scales=None), dict(k_scales=ks[:, :1]), dict(k_scales=ks.half()),
+                dict(q=q[0]), dict(q=q.transpose(2, 3)), dict(q=q[..., ::2]), dict(q=q.half()), dict(q=q.cpu()),
+                dict(out=torch.empty(3, device="cuda")), dict(out=q.half()), dict(lse=torch.empty_like(q)),
+                dict(out_dtype=torch.float16), dict(out_dtype="bf16"), dict(workspace=torch.empty(8)),
+                dict(selected=lens), dict(selected=torch.zeros((2, 2, 2), device="cuda"))):
+        with pytest.raises(ValueError):
+            call(**bad)
+    for bad in (dict(q=3), dict(k_pages=None), dict(page_table=[1]), dict(selected="x"), dict(workspace=7)):
+        with pytest.raises(TypeError):
+            call(**bad)
+    for bad, status in ((dict(q=q.float()), ra.RA_ERR_UNSUPPORTED), (dict(q=q[:, :, :3].contiguous()), ra.RA_ERR_INVALID_ARG),
+                        (dict(workspace=torch.empty(256, dtype=torch.uint8, device="cuda")), ra.RA_ERR_WORKSPACE),
+                        (dict(selected=torch.zeros((2, 2, 0), dtype=torch.int32, device="cuda")), ra.RA_ERR_INVALID_ARG)):
+        with pytest.raises(ra.RAError) as e:
+            call(**bad)
+        assert e.value.status == status
+    with pytest.raises(ra.RAError):
+        ra.ra_cache_read(kp, vp, table, lens, 0, k_scales=ks, v_scales=vs)
+    with pytest.raises(ValueError):
+        ra.ra_cache_read(kp, vp, table, lens, 1 << 40, k_scales=ks, v_scales=vs)
+    with pytest.raises(ValueError):
+        ra.ra_cache_append(q, q, kp, vp, table, lens, k_scales=ks, v_scales=vs)  # four heads for two
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
+def test_given_outputs_and_streams(cuda_lib):
+    """Outputs are written where they are given; on a given stream (object or handle)
+    the workspace belongs to that stream, so calls one after another do not share it
+    with the current stream's work."""
+    ra = cuda_lib
+    c = Case("bf16", 2, 2, 8, 2, 128, 32, [400, 900], seed=1)
+    want = ra.ra_paged_decode_attention(*c.args, out_dtype=torch.bfloat16, **c.kw)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        out = torch.empty_like(want[0])
+        lse = torch.empty_like(want[1])
+        torch.cuda.synchronize()
+        got = []
+        for _ in range(20):
+            got.append(ra.ra_paged_decode_attention(*c.args, stream=stream, out_dtype=torch.bfloat16, **c.kw))
+            torch.empty(16 << 20, dtype=torch.uint8, device="cuda").fill_(255)  # the current stream's allocations
+        r = ra.ra_paged_decode_attention(*c.args, stream=stream, out=out, lse=lse, **c.kw)
+        assert r[0].data_ptr() == out.data_ptr() and r[1].data_ptr() == lse.data_ptr()
+        torch.cuda.synchronize()
+        for g in got + [(out, lse)]:
+            assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1])
+
+
 def test_a_serving_run(cuda_lib):
     """Prompt, appended in chunks; then decoded token by token: the paged calls
     against the dense decode over the same (bf16) cache, and ra_ring_attention over
