@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_
   constexpr int J = D / 32;  // 16-byte chunks of a lane in lo, and in hi
   const int b = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 31;
   const int gr = lane >> 2, qd = lane & 3;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  chain_launches();
   for (int p0 = (blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5)) * 16; p0 < a.bt.max_pages;
        p0 += gridDim.x * (kScoreThreads / 32) * 16) {
     // lengths, table and queries are loaded side by side; the lengths say afterwards what counts
@@ -382,6 +382,7 @@ __device__ __forceinline__ Key kth_largest(SelectShared& sh, Each&& each, int wa
 template <int D>
 __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_constant__ SelectArgs a) {
   __shared__ SelectShared sh;
+  chain_launches();
   constexpr int L = D / 8, G = 32 / L;  // lanes of a page in an exact sum, pages side by side
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / a.bt.Hkv, h = blockIdx.x % a.bt.Hkv;
@@ -390,7 +391,6 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
   const int shift = a.bt.page_shift;
   const int pages = (s.len + (1 << shift) - 1) >> shift;
   const int n = first_new_page(s, shift), real = s.fresh * a.groups;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (pages <= a.n_sel) {  // every page
     for (int i = tid; i < a.n_sel; i += kSelThreads) out[i] = i < pages ? i : -1;
     return;

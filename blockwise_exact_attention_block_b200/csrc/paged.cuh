@@ -15,6 +15,16 @@ namespace ra {
 
 constexpr int kCacheBf16 = 0, kCacheI8 = 1, kCacheE4M3 = 2;  // template codes of the cache types
 
+// Every kernel of the paged cache is launched as a programmatic dependent of what
+// precedes it on the stream and begins with this: the next one may be brought
+// onto the SMs from here on, and nothing in global memory is read or written
+// until all that precedes has completed and is visible.  Every thread of every
+// CTA comes here, so a grid's completion implies that of the grids before it.
+__device__ __forceinline__ void chain_launches() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 struct PagedBatch {
   const int* page_table;  // [B][max_pages]
   const int* seq_lens;    // [B]
@@ -250,6 +260,7 @@ template <int D, int ET>
 __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
   __shared__ uint32_t s_lo[kAppendThreads / 32][D / 2], s_hi[kAppendThreads / 32][D / 2];
+  chain_launches();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / LPR, lr = lane % LPR;
   const int upc = (kAppendThreads / 32) / a.wpu, wi = warp % a.wpu;  // units per CTA, warp in the unit
@@ -414,6 +425,7 @@ __device__ __forceinline__ void octet_values(const Octet<ET>& o, float (&v)[8]) 
 template <int D, int ET, typename Tout>
 __global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int LPR = D / 8, RPW = 32 / LPR, N = kReadRows / RPW;
+  chain_launches();
   const int lane = threadIdx.x & 31;
   const int sub = lane / LPR, lr = lane % LPR;
   const long long unit = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);

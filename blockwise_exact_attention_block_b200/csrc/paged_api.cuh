@@ -57,20 +57,35 @@ PagedBatch batch_of(const ra_paged_cache* c, int T) {
   return b;
 }
 
+// Launch as a programmatic dependent of the stream's last kernel: see chain_launches.
+template <typename... P, typename... A>
+ra_status launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+
 template <int D>
 ra_status launch_append_d(const AppendArgs& a, int et, unsigned grid, cudaStream_t st) {
-  if (et == kCacheBf16) cache_append_kernel<D, kCacheBf16><<<grid, kAppendThreads, 0, st>>>(a);
-  else if (et == kCacheI8) cache_append_kernel<D, kCacheI8><<<grid, kAppendThreads, 0, st>>>(a);
-  else cache_append_kernel<D, kCacheE4M3><<<grid, kAppendThreads, 0, st>>>(a);
-  return cuda_status(cudaGetLastError());
+  if (et == kCacheBf16) return launch_chained(cache_append_kernel<D, kCacheBf16>, grid, kAppendThreads, 0, st, a);
+  if (et == kCacheI8) return launch_chained(cache_append_kernel<D, kCacheI8>, grid, kAppendThreads, 0, st, a);
+  return launch_chained(cache_append_kernel<D, kCacheE4M3>, grid, kAppendThreads, 0, st, a);
 }
 
 template <int D, typename Tout>
 ra_status launch_read_t(const ReadArgs& a, int et, unsigned grid, cudaStream_t st) {
-  if (et == kCacheBf16) cache_read_kernel<D, kCacheBf16, Tout><<<grid, 256, 0, st>>>(a);
-  else if (et == kCacheI8) cache_read_kernel<D, kCacheI8, Tout><<<grid, 256, 0, st>>>(a);
-  else cache_read_kernel<D, kCacheE4M3, Tout><<<grid, 256, 0, st>>>(a);
-  return cuda_status(cudaGetLastError());
+  if (et == kCacheBf16) return launch_chained(cache_read_kernel<D, kCacheBf16, Tout>, grid, 256, 0, st, a);
+  if (et == kCacheI8) return launch_chained(cache_read_kernel<D, kCacheI8, Tout>, grid, 256, 0, st, a);
+  return launch_chained(cache_read_kernel<D, kCacheE4M3, Tout>, grid, 256, 0, st, a);
 }
 
 constexpr int kPgMinRun = 1;  // shortest run of a team, in units of the line (5, two tiles: 17 us for 1,000 keys, against 12)
@@ -103,17 +118,8 @@ PagedPlan paged_plan(int B, int Tq, int Hq, int Hkv, int D) {
 template <int D, int COLS, int WPR, int NW>
 ra_status launch_paged_combine(const PagedArgs& a, int teams, cudaStream_t st) {
   const long long rows = static_cast<long long>(a.bt.B) * a.bt.Hkv * a.rows;
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + NW / WPR - 1) / (NW / WPR) * (D / COLS)), 1, 1);
-  cfg.blockDim = dim3(32 * NW, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, COLS, WPR, NW>, a, teams));
+  const long long grid = (rows + NW / WPR - 1) / (NW / WPR) * (D / COLS);
+  return launch_chained(paged_combine_kernel<D, COLS, WPR, NW>, static_cast<unsigned>(grid), 32 * NW, 0, st, a, teams);
 }
 
 template <int D, int ET, int NB, bool TEAMS>
@@ -134,8 +140,7 @@ ra_status launch_paged_t(const PagedArgs& a, cudaStream_t st) {
   const long long line = (tiles + kPgPairCost) * a.bt.B * a.bt.Hkv;
   const long long runs = (line + a.min_run - 1) / a.min_run;
   const int grid = static_cast<int>(runs < sm_count() ? runs : sm_count());
-  paged_partial_kernel<D, ET, NB, TEAMS><<<grid, SL::kThreads, SL::kBytes, st>>>(a);
-  const ra_status s = cuda_status(cudaGetLastError());
+  const ra_status s = launch_chained(paged_partial_kernel<D, ET, NB, TEAMS>, grid, SL::kThreads, SL::kBytes, st, a);
   if (s != RA_OK) return s;
   // a row's parts: 32 warps where the rows are few, one where they alone fill the GPU
   const long long rows = static_cast<long long>(a.bt.B) * a.bt.Hkv * a.rows;
@@ -173,20 +178,9 @@ ra_status launch_select_d(const SelectArgs& a, cudaStream_t st) {
   const long long pairs = static_cast<long long>(a.bt.B) * a.bt.Hkv;
   const long long need = (a.bt.max_pages + per - 1) / per, most = (32LL * sm_count() + pairs - 1) / pairs;
   const dim3 grid(static_cast<unsigned>(need < most ? need : most), a.bt.Hkv, a.bt.B);
-  page_score_kernel<D><<<grid, kScoreThreads, 0, st>>>(a);
-  const ra_status s = cuda_status(cudaGetLastError());
+  const ra_status s = launch_chained(page_score_kernel<D>, grid, kScoreThreads, 0, st, a);
   if (s != RA_OK) return s;
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(static_cast<unsigned>(a.bt.B) * a.bt.Hkv, 1, 1);
-  cfg.blockDim = dim3(kSelThreads, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, page_select_kernel<D>, a));
+  return launch_chained(page_select_kernel<D>, static_cast<unsigned>(pairs), kSelThreads, 0, st, a);
 }
 
 }  // namespace

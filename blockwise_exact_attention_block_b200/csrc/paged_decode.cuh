@@ -468,11 +468,6 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SL::kAbort);
   const int teams = SL::kWarps / a.R, slots = pg_slots<SL>(a.R);
 
-  // the combine kernel may be brought onto the SMs; it waits for this grid's end itself
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  long long own = 0;  // the walker's first lengths, on their way while the barriers are set up
-  if (warp == SL::kWarps && lane < a.bt.B) own = pg_units(a, seq_len_of(a.bt, lane));
-  if (tid == 32 * SL::kWarps) *abort_flag = grid_timed_out() ? 1 : 0;
   for (int i = tid; i < teams * slots; i += SL::kThreads) {
     mbar_init(sb + SL::kFull + 8u * i, 32 * a.R);  // every thread of the team
     mbar_init(sb + SL::kEmpty + 8u * i, a.R);
@@ -482,6 +477,10 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
     mbar_init(sb + SL::kQEmpty + 8u * i, a.R);
   }
   fence_mbar_init();
+  chain_launches();
+  long long own = 0;  // the walker's first lengths, on their way while the barriers are set up
+  if (warp == SL::kWarps && lane < a.bt.B) own = pg_units(a, seq_len_of(a.bt, lane));
+  if (tid == 32 * SL::kWarps) *abort_flag = grid_timed_out() ? 1 : 0;
   __syncthreads();
   if (*abort_flag) return;
   if (warp == SL::kWarps) {
@@ -954,7 +953,7 @@ __global__ void __launch_bounds__(32 * NW) paged_combine_kernel(const __grid_con
   const int col = COLS * (blockIdx.x % (D / COLS)) + kPer * lane;
   const long long id = static_cast<long long>(blockIdx.x / (D / COLS)) * (NW / WPR) + warp / WPR;
   const int w0 = warp % WPR;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  chain_launches();
   const long long pairs = static_cast<long long>(a.bt.B) * a.bt.Hkv;
   if (id >= pairs * a.rows) return;
   const long long pair = id / a.rows;
