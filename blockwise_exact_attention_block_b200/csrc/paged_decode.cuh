@@ -394,7 +394,6 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
       m.b = b;
       m.h = h;
       m.len = s.len;
-      const int fresh = s.fresh;
       int flags = kPgStop;  // the run's end
       if (work) {
         auto place = [&](int lg, int pg, int key, int& r, int& p) {
@@ -416,18 +415,8 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
         const bool owner = pair + kPgPairCost >= 0;
         const bool last = t + 1 == nt || pair + kPgPairCost + t + 1 >= n;
         flags = (first ? kPgFirst : 0) | (last ? kPgLast : 0) | (owner && t + 1 == nt ? kPgWhole : 0) | (owner ? kPgOwner : 0);
-        if (first && owner) {  // the pair's record: cut, if its last tile is another team's
-          const int on = static_cast<int>(static_cast<unsigned>(pair + kPgPairCost + nt - 1) / static_cast<unsigned>(run));
-          a.cut[static_cast<long long>(b) * a.bt.Hkv + h] =
-              on == 0 ? make_int2(-1, -1) : make_int2(static_cast<int>(u), static_cast<int>(u) + on);
-        }
-        first = last;
-        ++t;
-        settle();
-      } else {
-        stopped = true;
       }
-      m.fresh_flags = (fresh << 8) | flags;
+      m.fresh_flags = (s.fresh << 8) | flags;
       queue[slot] = m;
       mbar_arrive(qfull + 8u * slot);
       ++posted;
@@ -435,7 +424,20 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
         slot = 0;
         phase ^= 1u;
       }
-      if (work) look_up();
+      // what nobody waits for: the pair's record (cut, if its last tile is another team's) and the next tile
+      if (work) {
+        if ((flags & (kPgFirst | kPgOwner)) == (kPgFirst | kPgOwner)) {
+          const int on = static_cast<int>(static_cast<unsigned>(pair + kPgPairCost + nt - 1) / static_cast<unsigned>(run));
+          a.cut[static_cast<long long>(b) * a.bt.Hkv + h] =
+              on == 0 ? make_int2(-1, -1) : make_int2(static_cast<int>(u), static_cast<int>(u) + on);
+        }
+        first = flags & kPgLast;
+        ++t;
+        settle();
+        if (work) look_up();
+      } else {
+        stopped = true;
+      }
     }
     if (__all_sync(0xffffffffu, stopped)) return;
     if (__any_sync(0xffffffffu, go)) {
@@ -761,9 +763,13 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
           top = fmax3(fmax3(top, w[mb][nb][0], w[mb][nb][1]), w[mb][nb][2], w[mb][nb][3]);
         }
     };
-    if (masked) weigh(std::true_type{});
-    else weigh(std::false_type{});
-    if (__any_sync(0xffffffffu, top > kPgLazy)) {  // the first tile of a pair always comes here (E = -inf)
+    bool raise = flags & kPgFirst;  // (E = -inf there)
+    if (!raise) {
+      if (masked) weigh(std::true_type{});
+      else weigh(std::false_type{});
+      raise = __any_sync(0xffffffffu, top > kPgLazy);
+    }
+    if (raise) {
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
         float y = -INFINITY;  // largest x_j + log2 vs_j of the row's visible keys
