@@ -266,6 +266,9 @@ ra_status ra_paged_decode_attention(const void* q, ra_dtype in_dtype, const ra_p
   const PagedPlan p = paged_plan(cache->B, Tq, Hq, cache->Hkv, cache->D);
   if (!workspace || workspace_bytes < p.total) return RA_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return RA_ERR_INVALID_ARG;
+  // a team's run of the line (see launch_paged_t) is counted in 32 bits
+  const long long width = static_cast<long long>(cache->max_pages) * cache->page_size / kPgKeys + 1 + kPgPairCost;
+  if (width * cache->B >= (1LL << 30) * sm_count() / cache->Hkv) return RA_ERR_UNSUPPORTED;
   PagedArgs a;
   memset(&a, 0, sizeof(a));
   a.bt = batch_of(cache, Tq);

@@ -23,8 +23,9 @@
 // 2^-25 of the largest w.  One rounded term (2^-9 for bf16) would cost as much
 // accuracy as the output's own rounding.  8-bit codes are turned into f16, which
 // holds them exactly; the queries then go in as f16 too, scaled by a power of two
-// that brings the warp's largest to 2^14 (bf16's 8 bits fit, and what falls
-// under f16's range is below 2^-38 of the largest).
+// that brings the warp's largest to 2^14 (bf16's 8 bits fit down to 2^-30 of it).  A
+// warp whose rows differ by more than 2^16 scales each row by itself and brings
+// the scores to the largest's scale.
 //
 // Bound by HBM: a cached element meets the groups * Tq (<= 64) query rows of its
 // KV head and is used once.  So the cache is streamed once, through rings of
@@ -586,6 +587,8 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
 
   uint32_t qb[KS][NB][2];
   float o[KS][NB][4], E[NR], l[NR], qscale = a.scale_log2;
+  float rowscale[NR];  // (8-bit cache, `uneven`) this lane's rows' scales by the warp's
+  bool uneven = false;
   int lim[NR], minlim = 0;
   // lane parts of the shared-memory addresses; a chunk index goes in by exclusive or
   // (the slots begin at multiples of the 256 bytes that it can change)
@@ -609,9 +612,10 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
         E[i] = -INFINITY;
         l[i] = 0.f;
       }
-      float qmax = 0.f;
+      uint32_t qmax[NB];  // largest magnitudes, as pairs of bf16 bits
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
+        qmax[nb] = 0u;
         const int r = row0 + 8 * nb + gr, tk = r / a.groups;
         const bool real = r < a.rows && tk < fresh;
         const __nv_bfloat16* qr =
@@ -627,28 +631,53 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
                                  : make_uint2(0u, 0u);
             qb[ks][nb][0] = x.x;
             qb[ks][nb][1] = x.y;
-            qmax = fmaxf(qmax, fmaxf(fmaxf(fabsf(__uint_as_float(x.x << 16)), fabsf(__uint_as_float(x.x & 0xffff0000u))),
-                                     fmaxf(fabsf(__uint_as_float(x.y << 16)), fabsf(__uint_as_float(x.y & 0xffff0000u)))));
+            qmax[nb] = __vmaxu2(qmax[nb], __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu));
           }
         }
       }
 #pragma unroll
-      for (int x = 16; x; x >>= 1) {
-        minlim = min(minlim, __shfl_xor_sync(0xffffffffu, minlim, x));
-        if (ET != kCacheBf16) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, x));
-      }
+      for (int x = 16; x; x >>= 1) minlim = min(minlim, __shfl_xor_sync(0xffffffffu, minlim, x));
       if constexpr (ET != kCacheBf16) {
+        // exponent fields of the rows' largest values, and of the warp's; a row with an
+        // infinity or a NaN, whose result is NaN, counts for neither
+        int er[NB], ew = 0;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          uint32_t m = max(qmax[nb] & 0xffffu, qmax[nb] >> 16);
+#pragma unroll
+          for (int x = 1; x < 4; x <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, x));
+          er[nb] = m < 0x7f80u ? static_cast<int>(m >> 7) : 0;
+          ew = max(ew, er[nb]);
+        }
+        ew = __reduce_max_sync(0xffffffffu, ew);
+        bool low = false;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) low |= er[nb] > 0 && er[nb] + 16 < ew;
+        uneven = __any_sync(0xffffffffu, low);
         // 2^up brings the largest query to [2^14, 2^15), within what an fp32 factor can say
-        const int up = min(max(127 + 14 - static_cast<int>(__float_as_uint(qmax) >> 23), -110), 110);
-        const float mul = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+        const int up = min(127 + 14 - ew, 110);
+        float mul[NB];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) mul[nb] = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
         qscale = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+        if (uneven) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const int own = er[nb] > 0 ? min(127 + 14 - er[nb], 110) : up;
+            mul[nb] = __uint_as_float(static_cast<uint32_t>(127 + own) << 23);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)  // (2^-126 apart: as good as 0)
+              rowscale[2 * nb + e] = __uint_as_float(
+                  static_cast<uint32_t>(max(127 + up - __shfl_sync(0xffffffffu, own, 4 * (2 * qd + e)), 0)) << 23);
+          }
+        }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
             const uint32_t x = qb[ks][nb][0], y = qb[ks][nb][1];
-            const uint32_t xf = pack_f16x2(__uint_as_float(x << 16) * mul, __uint_as_float(x & 0xffff0000u) * mul);
-            const uint32_t yf = pack_f16x2(__uint_as_float(y << 16) * mul, __uint_as_float(y & 0xffff0000u) * mul);
+            const uint32_t xf = pack_f16x2(__uint_as_float(x << 16) * mul[nb], __uint_as_float(x & 0xffff0000u) * mul[nb]);
+            const uint32_t yf = pack_f16x2(__uint_as_float(y << 16) * mul[nb], __uint_as_float(y & 0xffff0000u) * mul[nb]);
             // int8 codes pair up as bytes 0, 2 and 1, 3; e4m3 ones as 0, 1 and 2, 3
             qb[ks][nb][0] = ET == kCacheI8 ? __byte_perm(xf, yf, 0x5410) : xf;
             qb[ks][nb][1] = ET == kCacheI8 ? __byte_perm(xf, yf, 0x7632) : yf;
@@ -713,6 +742,13 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
           }
         }
     }
+    if (ET != kCacheBf16 && uneven)
+#pragma unroll
+      for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mb][nb][e] *= rowscale[2 * nb + (e & 1)];
     release();
     if (odd) load_v();
     else load_k();
@@ -737,7 +773,9 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         vs[i] = scales[slot * kPgKeys + gr + 8 * i];
-        if (vs[i] == 0.f) vs[i] = 1.f;  // a row of zeros: its codes are 0, its weight still counts in l
+        // A row of zeros: its codes are 0 and its term counts in l alone.  It holds E near
+        // its score, or l would overflow, but must not crowd out the other weights' bits.
+        if (vs[i] == 0.f) vs[i] = 0x1p-80f;
       }
     }
     float w[2][NB][4], lt[NR], top;
@@ -779,7 +817,8 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
           for (int k8 = 0; k8 < 2; ++k8) {
             const int e = 2 * k8 + (i & 1);
             float x = s[mb][i >> 1][e] * xc[2 * mb + k8];
-            if constexpr (ET != kCacheBf16) x += __log2f(vs[2 * mb + k8]);
+            // (a scale below those that an append writes could make l overflow)
+            if constexpr (ET != kCacheBf16) x += fmaxf(__log2f(vs[2 * mb + k8]), -100.f);
             if ((seen >> (8 * mb + 4 * (i >> 1) + e)) & 1u) y = fmaxf(y, x);
           }
 #pragma unroll
@@ -803,7 +842,7 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
     bool slow = false;
     if (ET == kCacheBf16 && masked) {
       // A key that a row does not see may hold anything (old tokens, memory never
-      // written): 0 * NaN must not reach the sum.  Codes of 8 bits are finite.
+      // written): 0 * NaN must not reach the sum.
       uint32_t big = 0;
 #pragma unroll
       for (int c = 0; c < KS; ++c)
@@ -818,6 +857,26 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
           }
         }
       slow = __any_sync(0xffffffffu, big != 0);
+    }
+    if (ET == kCacheE4M3 && masked) {
+      // The same of e4m3, whose one magnitude without a value a visible row does not
+      // hold: it becomes 0 (a team's warps may all do so).  int8 codes are all finite.
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t at = vt + 16 * (lane + 32 * i);
+        uint32_t x[4], any = 0;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t nan = ((x[j] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // bit 7 of such bytes
+          any |= nan;
+          x[j] &= ~(nan | (nan - (nan >> 7)));
+        }
+        if (any)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
+                       : "memory");
+      }
+      __syncwarp();
     }
     if (!slow) {
 #pragma unroll

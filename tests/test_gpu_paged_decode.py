@@ -229,6 +229,83 @@ def test_scores_of_every_size(cuda_lib):
         c.check(ra.ra_paged_decode_attention(*c.args, out_dtype=torch.float32, **c.kw), True)
 
 
+@pytest.mark.parametrize("dtype", ["int8", "e4m3"])
+@pytest.mark.parametrize("B,Tq,Hq,Hkv,D,ps,seq", [(2, 1, 4, 2, 128, 16, [20, 90]), (1, 3, 12, 2, 64, 64, [41]),
+                                                  (3, 4, 32, 2, 128, 32, [70, 33, 7]), (1, 1, 8, 8, 64, 128, [130])])
+def test_masked_codes_may_be_any_byte(cuda_lib, dtype, B, Tq, Hq, Hkv, D, ps, seq):
+    """Memory never written holds every code, e4m3's without a value among them: the
+    result is, bit for bit, that with other bytes there."""
+    ra = cuda_lib
+    c = Case(dtype, B, Tq, Hq, Hkv, D, ps, seq, seed=11)
+    for causal in (True, False):
+        want = ra.ra_paged_decode_attention(*c.args, causal=causal, out_dtype=torch.float32, **c.kw)
+        c.check(want, causal)
+        for byte in (0x7f, 0xff, 0x80):
+            pages = {}
+            for w in "kv":
+                dead = torch.isnan(c.scales[w])[..., None]
+                raw = c.pages[w].view(torch.uint8)
+                pages[w] = torch.where(dead, torch.full_like(raw, byte), raw).view(TORCH[dtype])
+            kept = {w: x.clone() for w, x in pages.items()}
+            got = ra.ra_paged_decode_attention(c.args[0], pages["k"], pages["v"], *c.args[3:], causal=causal,
+                                               out_dtype=torch.float32, **c.kw)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), hex(byte)
+            for w in "kv":
+                assert torch.equal(pages[w].view(torch.uint8), kept[w].view(torch.uint8))
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "int8", "e4m3"])
+@pytest.mark.parametrize("Tq,Hq,D", [(1, 8, 128), (2, 8, 64), (7, 8, 128)])
+@pytest.mark.parametrize("factor", [2.0 ** 40, 2.0 ** 100, float("inf"), float("nan"), 2.0 ** -60])
+def test_rows_of_every_size_stand_side_by_side(cuda_lib, dtype, Tq, Hq, D, factor):
+    """A row's result does not hang on the others of its KV head: rows 2^40 or 2^100
+    larger, infinite ones, and rows so small that they weigh every key alike."""
+    ra = cuda_lib
+    c = Case(dtype, 2, Tq, Hq, 1, D, 32, [300, 77], seed=12)
+    odd = torch.zeros((2, Tq, Hq), dtype=torch.bool)
+    odd[:, :, 1::3] = True
+    c.q[odd] = (c.q[odd].float() * factor).to(torch.bfloat16)
+    got = ra.ra_paged_decode_attention(c.q.cuda(), *c.args[1:], out_dtype=torch.float32, **c.kw)
+    shown = ~odd if not factor < 1 else torch.ones_like(odd)
+    c.q[~shown] = 0.0  # the others' results are replaced by what a row of zeros has
+    ro, rl = c.expect(True)
+    out, lse = torch.tensor(ro, dtype=torch.float32), torch.tensor(rl, dtype=torch.float32)
+    out[shown], lse[shown] = got[0].cpu()[shown], got[1].cpu()[shown]
+    c.check((out, lse), True)
+    rest = got[0].cpu()[~shown]
+    if not math.isfinite(factor):
+        assert torch.isnan(rest).all()
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
+def test_value_scales_of_every_size(cuda_lib):
+    """Scales from subnormal ones to 2^100, and 0 beside others: the outputs are exact to a part of the
+    largest value, and lse does not hang on them."""
+    ra = cuda_lib
+    for dtype in ("int8", "e4m3"):
+        for exps in ((0,), (-97,), (100,), (-130,), (0, -40), (30, -30, 0)):
+            c = Case(dtype, 1, 1, 8, 2, 128, 16, [200], seed=13)
+            live = ~torch.isnan(c.scales["v"])
+            n = live.shape[2]
+            e = torch.tensor([exps[i % len(exps)] for i in range(n)], dtype=torch.float64)
+            s = (c.scales["v"].cpu().double() * torch.exp2(e)).float()
+            zero = [] if exps[0] < -80 else [5, 6]  # rows of zeros
+            s[:, :, zero] = torch.where(live[:, :, zero].cpu(), torch.zeros_like(s[:, :, zero]), s[:, :, zero])
+            c.scales["v"] = c.kw["v_scales"] = s.cuda()
+            was = np.where(c.ref.scale["v"] > 0, c.ref.scale["v"], 1.0)
+            c.ref.value["v"] = c.ref.value["v"] / was[..., None] * np.nan_to_num(f64(s))[..., None]
+            codes = c.pages["v"].view(torch.uint8).cpu()
+            codes[:, :, zero] = torch.where(live.cpu()[:, :, zero, None], torch.zeros_like(codes[:, :, zero]), codes[:, :, zero])
+            c.args = c.args[:2] + (codes.view(TORCH[dtype]).cuda(),) + c.args[3:]
+            got = ra.ra_paged_decode_attention(*c.args, out_dtype=torch.float32, **c.kw)
+            if exps[0] == -130:  # below fp32's normal numbers: no result but 0 is asked for, and the lse
+                assert (got[0].abs() < 2.0 ** -100).all()
+                got = (torch.tensor(c.expect(True)[0], dtype=torch.float32), got[1])
+            c.check(got, True, what=f"{dtype} {exps}")
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
 def test_offsets_past_32_bits(cuda_lib):
     """Pages whose byte and element offsets pass 2^32 and 2^31."""
     ra = cuda_lib
@@ -435,4 +512,32 @@ def test_a_serving_run(cuda_lib):
         got = ra.ra_paged_decode_attention(q[:, one].contiguous(), kp, vp, table, lens)
         want = ra.ra_decode_attention(q[:, one].contiguous(), k[:, :t + 1].contiguous(), v[:, :t + 1].contiguous())
         assert torch.allclose(got[0], want[0], atol=2e-2) and torch.allclose(got[1], want[1], atol=1e-4)
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
+@pytest.mark.parametrize("dtype", ["int8", "e4m3"])
+def test_zero_values_of_a_long_cache(cuda_lib, dtype):
+    """Every value 0 and scores that grow along the cache: outputs 0, lse that of the keys."""
+    ra = cuda_lib
+    n, D, ps = 300000, 64, 128
+    pages = -(-n // ps)
+    gen = torch.Generator().manual_seed(3)
+    k = torch.randn((pages, 1, ps, D), generator=gen)
+    k[..., 0] += torch.arange(pages * ps).view(pages, 1, ps) / n * 8
+    q = torch.zeros((1, 1, 1, D))
+    q[..., 0] = 30.0
+    kp, ks = torch.zeros((pages, 1, ps, D), dtype=TORCH[dtype]).cuda(), torch.zeros((pages, 1, ps)).cuda()
+    vp, vs = torch.zeros_like(kp), torch.zeros_like(ks)
+    table = torch.arange(pages, dtype=torch.int32)[None].cuda()
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    rows = k.permute(1, 0, 2, 3).reshape(1, pages * ps, 1, D)[:, :n].to(torch.bfloat16).cuda()
+    ra.ra_cache_append(rows, torch.zeros_like(rows), kp, vp, table, lens, k_scales=ks, v_scales=vs)
+    out, lse = ra.ra_paged_decode_attention(q.to(torch.bfloat16).cuda(), kp, vp, table, lens, k_scales=ks, v_scales=vs)
+    assert not out.any() and not vs.any()
+    back, _ = ra.ra_cache_read(kp, vp, table, lens, n, k_scales=ks, v_scales=vs, out_dtype=torch.float32)
+    x = back[0, :, 0, 0].double() * 30.0 / math.sqrt(D)
+    want = float(torch.logsumexp(x, 0))
+    # scores to (D + 4) 2^-24 of their largest, a sum of n terms, the exponentials
+    tol = (D + 4) * 2.0 ** -24 * float(x.abs().max()) + n * 2.0 ** -24 + 2.0 ** -20 * want
+    assert abs(float(lse) - want) <= tol
     assert ra.ra_get_device_status() == ra.RA_OK

@@ -113,6 +113,13 @@ def test_paged_decode_refuses(ra, kw, status):
     assert decode(ra, cache(ra), **kw) == status
 
 
+def test_paged_decode_refuses_a_line_past_32_bits(ra):
+    """Tiles of all (sequence, KV head) pairs by the table's width: a team's share of them is a 32-bit count."""
+    wide = dict(page_size=128, n_pages=1000, max_pages=1 << 23)  # 2^25 tiles each
+    assert decode(ra, cache(ra, B=1 << 14, Hkv=2, **wide)) == 2
+    assert decode(ra, cache(ra, B=1 << 20, Hkv=8, page_size=64, max_pages=1 << 24)) == 2
+
+
 def test_paged_decode_workspace(ra):
     # teams of a full grid: 8 warps an SM at least, 1, 2 or 4 to a team; two cut pairs each
     for Tq, Hq, Hkv, per in ((1, 8, 2, 8), (4, 32, 8, 8), (5, 4, 1, 4), (1, 64, 1, 2)):
