@@ -283,12 +283,6 @@ __device__ __forceinline__ void bwd_flush_row(uint32_t taddr, float* dst, bool v
   }
 }
 
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // One 32-column chunk of a row: from fp32 scores s and dP (raw TMEM bits) to
 // bf16 pairs of P = 2^(s * ss - lse2) and dS = P (dP - Delta), two columns per
 // packed fp32x2 operation.  nl / nd: -lse2 and -Delta per column (COLS) or

@@ -73,95 +73,93 @@ __device__ __forceinline__ float e4m3_value(uint32_t c) {
   return __uint_as_float(c << 20) * 0x1p120f;
 }
 
-// Code of x (|x| <= m s up to rounding) in int8 with scale s: the integer
-// nearest to the exact x / s, ties to even.  x * inv is within a few ulp of
-// the quotient, so only a neighbour of the rounded product can be nearer; the
-// remainder x - q s is exact in fp32 (x has 8 significant bits, |x - q s| is at
-// most about s / 2 and a multiple of s's last bit), so the comparison with
-// s / 2 decides every case as infinite precision would.
-__device__ __forceinline__ uint32_t quant_i8(float x, float s, float inv) {
-  float q = rintf(x * inv);
-  const float r = fmaf(-q, s, x);
-  const float half = 0.5f * s;
-  if (fabsf(r) >= half) {  // past the border, or on it
-    const float up = r > 0.f ? 1.f : -1.f;
-    if (fabsf(r) > half || (static_cast<int>(q) & 1)) q += up;
-  }
-  return static_cast<uint32_t>(static_cast<int>(q)) & 0xffu;
-}
-
-// The same for e4m3: the conversion of x * inv is the answer or a neighbour of it;
-// the exact remainders of the two candidates decide, ties to the even code.
-__device__ __forceinline__ uint32_t quant_e4m3(float x, float s, float inv) {
-  const float ax = fabsf(x);
-  uint16_t pair;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pair) : "f"(0.f), "f"(ax * inv));
-  uint32_t c = pair & 0xffu;
-  const float r = fmaf(-e4m3_value(c), s, ax);
-  const uint32_t other = r > 0.f ? min(c + 1u, 126u) : (c > 0u ? c - 1u : 0u);
-  const float r2 = fabsf(fmaf(-e4m3_value(other), s, ax)), r1 = fabsf(r);
-  if (r2 < r1 || (r2 == r1 && (c & 1u))) c = other;
-  return c | (x < 0.f ? 0x80u : 0u);
-}
-
-__device__ __forceinline__ uint32_t e4m3_quad(float a, float b, float c, float d) {
+__device__ __forceinline__ uint32_t e4m3_quad(uint64_t lo, uint64_t hi) {  // codes of two fp32 pairs
+  float2 l, h;
+  f2_unpack(lo, l.x, l.y);
+  f2_unpack(hi, h.x, h.y);
   uint32_t r;
   asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
       "mov.b32 %0, {l, h};\n\t}"
       : "=r"(r)
-      : "f"(a), "f"(b), "f"(c), "f"(d));
+      : "f"(l.x), "f"(l.y), "f"(h.x), "f"(h.y));
   return r;
 }
 
-// Eight bf16 values (pairs in u) of a row with scale s as codes.  Nearly all octets
-// have no value near a border between two codes; those take the short way:
-//   int8: x * inv + 1.5 2^23 in one fma rounds the product to the integer in the
-//   sum's low bits (the conversion instructions run at a quarter of the fma
-//   rate); the exact remainders of all eight must stay below s / 2.
-//   e4m3: with inv within 2^-22 of 1 / s, x (1 - 2^-21) inv and x (1 + 2^-21) inv lie
-//   on either side of x / s even after their own rounding; the conversion is
-//   monotonic, so where both give the same code it is the quotient's.
-// The others go value by value.
+// An 8-bit row's scale s = fp32(a / m), a its largest magnitude and m = 127 or 448,
+// and the factor `inv` with which quant_octet finds the code nearest to x / s for
+// every value x of the row, although s is rounded and so is x * inv.
+//
+// x and a have 8 significant bits.  x m / a, the quotient were s not rounded, is
+// then either exactly on a border between two codes (k + 1/2 for int8, 5 bits for
+// e4m3) or at least 2^-16 (int8: 254 |x| against an 8-bit odd number times a, both
+// integers of at most 64770) or 2^-13 (e4m3) of itself away from any.  x / s differs
+// from it by 2^-24 of itself, which way is the same for the whole row.  So:
+//   s too small (x / s beyond x m / a): inv is 1 / s made larger by 2^-18, too large:
+//   smaller.  That is more than the errors of inv and of the product, so a value on
+//   a border goes to its side, and too little to carry any other over a border.
+//   s exact, m = 127: then a's 8 bits are 254 and s is a power of two, and so is inv;
+//   the product is exact and a border goes to the even code by itself.
+//   s exact, m = 448 (a divisible by 7): inv is 1 / s to a few ulp and quant_octet
+//   rounds the product to 16 bits, which a border's 5 survive (`snap`).
+struct RowScale {
+  float s, inv;
+  bool snap;
+};
+
+// fp32(a / m) for a >= 2^-100 by the division with a divisor known in advance of
+// Brisebarre, Muller and Raina (IEEE Trans. Computers 2004): the product with the
+// rounded 1 / m, its exact remainder, and the remainder's product added back.  That it
+// is the correctly rounded quotient for every such a is checked value by value in
+// the tests, and so are the codes of every x for every a.
 template <int ET>
-__device__ __forceinline__ uint2 quant_octet(const uint32_t (&u)[4], float s, float inv) {
-  float x[8];
+__device__ __forceinline__ RowScale scale_of(float a) {
+  constexpr float m = ET == kCacheI8 ? 127.f : 448.f, r = static_cast<float>(1.0 / m);
+  RowScale o;
+  const float q = a * r;
+  o.s = fmaf(fmaf(-q, m, a), r, q);
+  const float rest = fmaf(-o.s, m, a);  // exact: positive when s is too small
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(o.inv) : "f"(o.s));
+  o.snap = rest == 0.f;
+  if (!o.snap) o.inv *= rest > 0.f ? 1.f + 0x1p-18f : 1.f - 0x1p-18f;
+  return o;
+}
+
+// An fp32 value's bits rounded to 16 significant ones.
+__device__ __forceinline__ float to_16_bits(uint32_t x) { return __uint_as_float((x + 0x80u) & 0xffffff00u); }
+
+// Eight bf16 values (pairs in u) of a row as codes: see RowScale.  int8: x * inv +
+// 1.5 2^23 in one fma rounds the product to the integer in the sum's low bits (the
+// conversion instructions run at a quarter of the fma rate).
+template <int ET>
+__device__ __forceinline__ uint2 quant_octet(const uint32_t (&u)[4], const RowScale& rs) {
+  const uint64_t inv = f2_pack(rs.inv, rs.inv);
+  uint64_t x[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-  }
-  uint32_t code[2];
-  bool plain;
+  for (int i = 0; i < 4; ++i) x[i] = f2_pack(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+  uint32_t c[2];
   if constexpr (ET == kCacheI8) {
+    const uint64_t magic = f2_pack(12582912.f, 12582912.f);
     uint32_t y[8];
-    float worst = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float t = fmaf(x[i], inv, 12582912.f);
-      y[i] = __float_as_uint(t);
-      worst = fmaxf(worst, fabsf(fmaf(-(t - 12582912.f), s, x[i])));
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t t = f2_fma(x[i], inv, magic);
+      y[2 * i] = static_cast<uint32_t>(t);
+      y[2 * i + 1] = static_cast<uint32_t>(t >> 32);
     }
-    plain = worst < 0.5f * s;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      code[i] = __byte_perm(__byte_perm(y[4 * i], y[4 * i + 1], 0x0040), __byte_perm(y[4 * i + 2], y[4 * i + 3], 0x0040), 0x5410);
+      c[i] = __byte_perm(__byte_perm(y[4 * i], y[4 * i + 1], 0x0040), __byte_perm(y[4 * i + 2], y[4 * i + 3], 0x0040), 0x5410);
   } else {
-    const float below = inv * (1.f - 0x1p-21f), above = inv * (1.f + 0x1p-21f);
-    uint32_t differ = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      code[i] = e4m3_quad(x[4 * i] * below, x[4 * i + 1] * below, x[4 * i + 2] * below, x[4 * i + 3] * below);
-      differ |= code[i] ^ e4m3_quad(x[4 * i] * above, x[4 * i + 1] * above, x[4 * i + 2] * above, x[4 * i + 3] * above);
-    }
-    plain = differ == 0u;
-  }
-  if (!plain) {
-    code[0] = code[1] = 0u;
+    for (int i = 0; i < 4; ++i) x[i] = f2_mul(x[i], inv);
+    if (rs.snap)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      code[i >> 2] |= (ET == kCacheI8 ? quant_i8(x[i], s, inv) : quant_e4m3(x[i], s, inv)) << (8 * (i & 3));
+      for (int i = 0; i < 4; ++i)
+        x[i] = f2_pack(to_16_bits(static_cast<uint32_t>(x[i])), to_16_bits(static_cast<uint32_t>(x[i] >> 32)));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) c[i] = e4m3_quad(x[2 * i], x[2 * i + 1]);
   }
-  return make_uint2(code[0], code[1]);
+  return make_uint2(c[0], c[1]);
 }
 
 // Eight bf16 values as fp32.
@@ -206,18 +204,6 @@ struct AppendArgs {
 constexpr int kAppendThreads = 256;
 constexpr int kAppendBatch = 2;  // rows of K and V a lane holds in flight
 
-// fp32(a / m), m = 127 or 448, for a >= 2^-100 with 8 significant bits, by the
-// division with a divisor known in advance of Brisebarre, Muller and Raina (IEEE
-// Trans. Computers 2004): the product with the rounded 1 / m, its exact
-// remainder, and the remainder's product added back.  That it is the correctly
-// rounded quotient for every such a is checked value by value in the tests.
-template <int ET>
-__device__ __forceinline__ float scale_of(float a) {
-  constexpr float m = ET == kCacheI8 ? 127.f : 448.f, r = static_cast<float>(1.0 / m);
-  const float q = a * r;
-  return fmaf(fmaf(-q, m, a), r, q);
-}
-
 // One row's octet of this lane into the cache: bits, or codes and the row's
 // scale (largest magnitude over the LPR lanes of the row).  bf16 magnitudes
 // compare as integers, a NaN or an infinity above every finite value.
@@ -235,15 +221,14 @@ __device__ __forceinline__ void append_row(const uint4& w, bool act, int lane_in
     am = max(am & 0xffffu, am >> 16);
 #pragma unroll
     for (int o = 1; o < LPR; o <<= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
-    float s = 0.f, inv = 0.f;
-    if (am >= 0x7f80u) {
-      s = __uint_as_float(0x7fc00000u);  // NaN: the row reads back as NaN
-    } else if (__uint_as_float(am << 16) >= 0x1p-100f) {
-      s = scale_of<ET>(__uint_as_float(am << 16));
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));  // near enough: see quant_octet
+    const float largest = __uint_as_float(am << 16);
+    const RowScale rs = scale_of<ET>(largest);
+    uint2 code = quant_octet<ET>(u, rs);
+    float s = rs.s;
+    if (!(largest >= 0x1p-100f && largest < INFINITY)) {  // too small, or NaN: then the row reads back as NaN
+      s = largest < 1.f ? 0.f : __uint_as_float(0x7fc00000u);
+      code = make_uint2(0u, 0u);
     }
-    uint2 code = make_uint2(0u, 0u);
-    if (inv != 0.f) code = quant_octet<ET>(u, s, inv);
     if (act) {
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pages) + row * D + 8 * lane_in_row) = code;
       if (lane_in_row == 0) scales[row] = s;

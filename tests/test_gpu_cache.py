@@ -147,6 +147,34 @@ def test_append_rounds_as_exact_arithmetic(cuda_lib, dtype, D):
 
 
 @pytest.mark.parametrize("dtype", ["int8", "e4m3"])
+def test_every_significand_against_every_scale(cuda_lib, dtype):
+    """Codes of all bf16 significands, over 20 binades, in rows of all largest significands: what
+    the choice between two codes can hang on, for the smallest scales, ordinary and the largest."""
+    ra = cuda_lib
+    D, ps = 128, 128
+    m = torch.arange(128, 256, dtype=torch.float64)
+    x = torch.cat([m * 2.0 ** -d for d in range(20)])                       # 2,560 values
+    x = x * torch.where(torch.arange(len(x)) % 2 == 0, 1.0, -1.0)
+    x = torch.cat([x, x.new_zeros(-len(x) % (D - 1))]).view(-1, D - 1)      # 21 rows
+    rows = torch.zeros((128, len(x), D), dtype=torch.float64)
+    rows[:, :, 0] = m[:, None]
+    rows[:, :, 1:] = torch.where(x.abs() <= m[:, None, None], x, 0.0)
+    rows = rows.view(-1, D)
+    k = torch.cat([(rows * 2.0 ** e).to(torch.bfloat16) for e in (-107, -7, 120)])[None, :, None]
+    T = k.shape[1]
+    table = torch.arange(-(-T // ps), dtype=torch.int32)[None].contiguous()
+    dev = Device(table.numel(), 1, ps, D, dtype, bounds=False)
+    ra.ra_cache_append(k.cuda(), -k.cuda(), dev.k, dev.v, table.cuda(), torch.tensor([T], dtype=torch.int32).cuda(), **dev.kw())
+    for got, scales, sign in ((dev.k, dev.ks, 1.0), (dev.v, dev.vs, -1.0)):
+        code, value, scale = P.quantise(sign * f64(k[0, :, 0]), dtype)
+        assert np.array_equal(f64(scales.view(-1)[:T]), scale)
+        got = f64(got.view(-1, D)[:T].float())
+        off = got != value / scale[:, None]
+        assert not off.any(), f"{off.sum()} codes, first {np.argwhere(off)[0]}"
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
+@pytest.mark.parametrize("dtype", ["int8", "e4m3"])
 def test_every_scale_is_correctly_rounded(cuda_lib, dtype):
     """All bf16 magnitudes from 2^-100 up as a row's largest value."""
     ra = cuda_lib
