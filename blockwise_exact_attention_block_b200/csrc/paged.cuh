@@ -41,13 +41,14 @@ struct SeqLen {
 __device__ __forceinline__ SeqLen seq_len_of(const PagedBatch& a, int b) {
   SeqLen s;
   s.len = a.seq_lens[b];
+  const int given = a.new_lens ? a.new_lens[b] : 0;  // (both loads before the first check)
   const int cap = a.max_pages << a.page_shift;
   if (s.len < 0 || s.len > cap) {
     set_status(RA_ERR_DEVICE_BOUNDS);
     s.len = min(max(s.len, 0), cap);
   }
   const int most = min(a.T, s.len);
-  s.fresh = a.new_lens ? a.new_lens[b] : most;
+  s.fresh = a.new_lens ? given : most;
   if (s.fresh < 0 || s.fresh > most) {
     set_status(RA_ERR_DEVICE_BOUNDS);
     s.fresh = min(max(s.fresh, 0), most);
@@ -201,7 +202,7 @@ struct AppendArgs {
   long long units;        // B * span * Hkv
 };
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;  // (256: 35.2 us for 24,000 int8 tokens of 8 heads, against 34)
 constexpr int kAppendBatch = 2;  // rows of K and V a lane holds in flight
 
 // One row's octet of this lane into the cache: bits, or codes and the row's
@@ -242,7 +243,7 @@ __device__ __forceinline__ void append_row(const uint4& w, bool act, int lane_in
 // warp and step, kAppendBatch steps' loads in flight.  The column minima and
 // maxima of the keys stay in registers until the unit's end.
 template <int D, int ET>
-__global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
   __shared__ uint32_t s_lo[kAppendThreads / 32][D / 2], s_hi[kAppendThreads / 32][D / 2];
   chain_launches();
@@ -251,6 +252,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const _
   const int upc = (kAppendThreads / 32) / a.wpu, wi = warp % a.wpu;  // units per CTA, warp in the unit
   const long long unit = static_cast<long long>(blockIdx.x) * upc + warp / a.wpu;
   int page = -1, r0 = 0, r1 = 0, h = 0, b = 0, tok0 = 0;
+  bool good = false;  // rows to write, and a page for them
   if (unit < a.units) {
     h = static_cast<int>(unit % a.bt.Hkv);
     const long long bj = unit / a.bt.Hkv;
@@ -262,7 +264,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const _
     const int logical = (begin >> a.bt.page_shift) + j;
     const long long first = static_cast<long long>(logical) << a.bt.page_shift;  // position of the page's row 0
     if (s.fresh > 0 && first < s.len) {
-      page = page_of(a.bt, b, logical);
+      // (not looked at before the first rows are on their way: the loads overlap)
+      page = a.bt.page_table[static_cast<long long>(b) * a.bt.max_pages + logical];
       r0 = max(begin - static_cast<int>(first), 0);
       r1 = min(s.len - static_cast<int>(first), ps);
       tok0 = static_cast<int>(first) - begin;  // token of the page's row 0 (may be negative)
@@ -271,8 +274,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const _
   // pairs of columns; min and max of bf16 pass over a NaN
   uint32_t lo[4] = {0x7f807f80u, 0x7f807f80u, 0x7f807f80u, 0x7f807f80u};
   uint32_t hi[4] = {0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u};
-  if (page >= 0) {
-    const long long prow = (static_cast<long long>(page) * a.bt.Hkv + h) << a.bt.page_shift;
+  if (r0 < r1) {
     const int step = a.wpu * RPW;
     for (int rb = r0 + wi * RPW; rb < r1; rb += step * kAppendBatch) {
       uint4 kw[kAppendBatch], vw[kAppendBatch];
@@ -286,11 +288,13 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const _
           vw[u] = __ldcs(reinterpret_cast<const uint4*>(a.v + src));
         }
       }
+      good = page >= 0 && page < a.bt.n_pages;
+      const long long prow = (static_cast<long long>(page) * a.bt.Hkv + h) << a.bt.page_shift;
 #pragma unroll
       for (int u = 0; u < kAppendBatch; ++u) {
         if (rb + u * step >= r1) break;  // the same for the whole warp
         const int r = rb + u * step + sub;
-        const bool act = r < r1;
+        const bool act = r < r1 && good;
         append_row<D, ET>(kw[u], act, lr, a.k_pages, a.k_scales, prow + r);
         append_row<D, ET>(vw[u], act, lr, a.v_pages, a.v_scales, prow + r);
         if (a.bounds && act) {
@@ -304,6 +308,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const _
       }
     }
   }
+  if (r0 < r1 && wi == 0 && lane == 0 && !good) set_status(RA_ERR_DEVICE_BOUNDS);
   if (a.bounds == nullptr) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -328,7 +333,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const _
           hi[i] = bf16x2_max(hi[i], s_hi[warp + w][4 * lr + i]);
         }
   }
-  if (page < 0 || wi != 0 || sub != 0) return;
+  if (!good || wi != 0 || sub != 0) return;
   uint4* bl = reinterpret_cast<uint4*>(a.bounds + (static_cast<long long>(page) * a.bt.Hkv + h) * 2 * D) + lr;
   if (r0 > 0) {  // earlier tokens' bounds stand in the page
     const uint4 x = bl[0], y = bl[D / 8];
@@ -351,11 +356,15 @@ struct ReadArgs {
   const void* pages[2];    // K, V
   const float* scales[2];
   void* out[2];            // null: not asked for
-  int groups;              // 16-row groups of T
+  int groups;              // groups of read_rows(D) rows of T
   long long units;         // B * groups * Hkv
 };
 
-constexpr int kReadRows = 16;  // output rows of a warp
+constexpr int kReadThreads = 128;
+// Output rows of a warp: 1,024 values of K and of V.  Small CTAs of short warps keep
+// loads and stores mixed on every SM (4 x 24,000 int8 tokens of 8 heads to bf16: 16 rows
+// in CTAs of 256 threads 98 us, of 128 90; 8 rows in 128 87, 95 % of the copy rate).
+__host__ __device__ constexpr int read_rows(int D) { return 1024 / D; }
 
 // One row's octet of a lane as it is stored, with its scale, and as fp32 values.
 template <int ET>
@@ -404,12 +413,12 @@ __device__ __forceinline__ void octet_values(const Octet<ET>& o, float (&v)[8]) 
   }
 }
 
-// A warp takes 16 consecutive tokens of one KV head (runs of 16 rows of a page
-// to read, heads side by side in the CTA to write); D / 8 lanes hold a row.  Keys
-// and values of all 16 are loaded before the first is written.
+// A warp takes consecutive tokens of one KV head (rows of a page side by side to
+// read, heads side by side in the CTA to write); D / 8 lanes hold a row.  Keys and
+// values of all its tokens are loaded before the first is written.
 template <int D, int ET, typename Tout>
-__global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__ ReadArgs a) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, N = kReadRows / RPW;
+__global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_constant__ ReadArgs a) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR, kRows = read_rows(D), N = kRows / RPW;
   chain_launches();
   const int lane = threadIdx.x & 31;
   const int sub = lane / LPR, lr = lane % LPR;
@@ -418,15 +427,15 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__
   const int h = static_cast<int>(unit % a.bt.Hkv);
   const long long bg = unit / a.bt.Hkv;
   const int g = static_cast<int>(bg % a.groups), b = static_cast<int>(bg / a.groups);
-  const int t0 = g * kReadRows;
-  // lane i < 16: the cache row of output row t0 + i, -1 where there is none.  The
+  const int t0 = g * kRows;
+  // lane i < kRows: the cache row of output row t0 + i, -1 where there is none.  The
   // table entry is loaded beside the length that says whether it counts.
-  const long long pos = static_cast<long long>(a.first) + t0 + (lane & (kReadRows - 1));
+  const long long pos = static_cast<long long>(a.first) + t0 + (lane & (kRows - 1));
   const long long logical = min(pos >> a.bt.page_shift, static_cast<long long>(a.bt.max_pages - 1));
   const int page = a.bt.page_table[static_cast<long long>(b) * a.bt.max_pages + logical];
   const int len = seq_len_of(a.bt, b).len;
   long long mine = -1;
-  if (lane < kReadRows && pos < len) {
+  if (lane < kRows && pos < len) {
     if (page >= 0 && page < a.bt.n_pages)
       mine = ((static_cast<long long>(page) * a.bt.Hkv + h) << a.bt.page_shift) + (pos & ((1 << a.bt.page_shift) - 1));
     else

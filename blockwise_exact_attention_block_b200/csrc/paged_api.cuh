@@ -83,9 +83,9 @@ ra_status launch_append_d(const AppendArgs& a, int et, unsigned grid, cudaStream
 
 template <int D, typename Tout>
 ra_status launch_read_t(const ReadArgs& a, int et, unsigned grid, cudaStream_t st) {
-  if (et == kCacheBf16) return launch_chained(cache_read_kernel<D, kCacheBf16, Tout>, grid, 256, 0, st, a);
-  if (et == kCacheI8) return launch_chained(cache_read_kernel<D, kCacheI8, Tout>, grid, 256, 0, st, a);
-  return launch_chained(cache_read_kernel<D, kCacheE4M3, Tout>, grid, 256, 0, st, a);
+  if (et == kCacheBf16) return launch_chained(cache_read_kernel<D, kCacheBf16, Tout>, grid, kReadThreads, 0, st, a);
+  if (et == kCacheI8) return launch_chained(cache_read_kernel<D, kCacheI8, Tout>, grid, kReadThreads, 0, st, a);
+  return launch_chained(cache_read_kernel<D, kCacheE4M3, Tout>, grid, kReadThreads, 0, st, a);
 }
 
 constexpr int kPgMinRun = 1;  // shortest run of a team, in units of the line (5, two tiles: 17 us for 1,000 keys, against 12)
@@ -205,8 +205,8 @@ ra_status ra_cache_append(const ra_paged_cache* cache, const void* k, const void
   a.bounds = static_cast<__nv_bfloat16*>(cache->key_bounds);
   const int ps = cache->page_size;
   a.span = page_span(T, ps);
-  a.wpu = 1;  // about 16 rows for each warp of a unit
-  while (a.wpu * 16 < ps && a.wpu * 16 < T) a.wpu *= 2;
+  a.wpu = 1;  // about 16 rows for each warp of a unit, a CTA's warps at most
+  while (a.wpu * 16 < ps && a.wpu * 16 < T && a.wpu < kAppendThreads / 32) a.wpu *= 2;
   a.units = static_cast<long long>(cache->B) * a.span * cache->Hkv;
   const int upc = (kAppendThreads / 32) / a.wpu;
   const long long grid = (a.units + upc - 1) / upc;
@@ -235,9 +235,9 @@ ra_status ra_cache_read(const ra_paged_cache* cache, int first, int T, void* k, 
   a.scales[1] = cache->v_scales;
   a.out[0] = k;
   a.out[1] = v;
-  a.groups = (T - 1) / kReadRows + 1;
+  a.groups = (T - 1) / read_rows(cache->D) + 1;
   a.units = static_cast<long long>(cache->B) * a.groups * cache->Hkv;
-  const long long grid = (a.units + 7) / 8;
+  const long long grid = (a.units - 1) / (kReadThreads / 32) + 1;
   if (grid > 0x7fffffffLL) return RA_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int et = cache_code(cache->dtype);
