@@ -156,6 +156,14 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// Closes the group of this thread's copies since the last one (it may be empty), and
+// waits for all groups but the last N.
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // D (16x8 fp32) += A (16x16, row-major) * B (16x8, column-major), operands bf16
@@ -469,9 +477,9 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SL::kAbort);
-  const int teams = SL::kWarps / a.R, slots = pg_slots<SL>(a.R);
+  const int teams = SL::kWarps / a.R, slots = TEAMS ? pg_slots<SL>(a.R) : SL::kSlots;
 
-  for (int i = tid; i < teams * slots; i += SL::kThreads) {
+  for (int i = tid; TEAMS && i < teams * slots; i += SL::kThreads) {
     mbar_init(sb + SL::kFull + 8u * i, 32 * a.R);  // every thread of the team
     mbar_init(sb + SL::kEmpty + 8u * i, a.R);
   }
@@ -525,6 +533,8 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
   int lslot = 0, lq = 0, lr0 = 0, lr1 = 0;  // next slot and queue entry, rows of the tile being loaded
   uint32_t lphase = 0, lqphase = 0;
   bool lstop = false, wrapped = false, ok = true;
+  int slot = 0;  // and the slot to be read
+  uint32_t phase = 0;
   auto copy_item = [&](const uint8_t* src, const float* sc) {
     if (TEAMS && wrapped) ok &= mbar_wait(empty + 8u * lslot, lphase ^ 1u, abort_flag);  // (one warp: it has read the slot)
     const uint8_t* g0 = src + static_cast<long long>(lr0) * ROW;
@@ -544,14 +554,25 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
     if constexpr (ET != kCacheBf16)
       if (rt == 0 && lane < 8)
         copy16(sb + SL::kScale + (slot0 + lslot) * kPgKeys * 4 + 16 * lane, sc + (lane < 4 ? lr0 : lr1 - 16) + 4 * lane);
-    copies_arrive(full + 8u * lslot);
+    if (TEAMS) copies_arrive(full + 8u * lslot);
     if (++lslot == slots) {
       lslot = 0;
       lphase ^= 1u;
       wrapped = true;
     }
   };
-  auto load_k = [&]() {  // the next queued tile's keys, if there is a tile
+  // A warp on its own counts groups of copies: one for each item, empty behind the
+  // last tile, so that `slots` of them are always open and the oldest is the next to
+  // be read.  A team's warps wait for one another's copies on barriers.
+  auto landed = [&]() {
+    if constexpr (TEAMS) {
+      ok &= mbar_wait(full + 8u * slot, phase, abort_flag);
+    } else {
+      copies_wait<SL::kSlots - 1>();
+      __syncwarp();
+    }
+  };
+  auto next_k = [&]() {  // the next queued tile's keys, if there is a tile
     if (lstop) return;
     ok &= mbar_wait(qfull + 8u * lq, lqphase, abort_flag);
     const int4 rows = *reinterpret_cast<const int4*>(&queue[lq]);
@@ -565,11 +586,15 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
     }
     copy_item(src_k, a.k_scales);
   };
+  auto load_k = [&]() {
+    next_k();
+    if (!TEAMS) copies_commit();
+  };
   auto load_v = [&]() {  // and its values
     if (!lstop) copy_item(src_v, a.v_scales);
+    if (!TEAMS) copies_commit();
   };
-  int slot = 0, cq = 0;
-  uint32_t phase = 0;
+  int cq = 0;
   auto release = [&]() {  // this warp has read the slot
     __syncwarp();
     if (TEAMS && lane == 0) mbar_arrive(empty + 8u * slot);
@@ -578,6 +603,7 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
       phase ^= 1u;
     }
   };
+  static_assert(SL::kSlots <= 2 * (kPgQueue - 2), "the queue covers a warp's ring");
   const bool odd = slots & 1;  // then a released K slot takes a V, and the other way round
   load_k();
   for (int i = 1; i < slots; ++i) {
@@ -690,7 +716,7 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
     }
 
     // ---- scores: s[mb][nb] holds keys 16 mb + gr, + 8 and rows 8 nb + 2 qd, + 1
-    ok &= mbar_wait(full + 8u * slot, phase, abort_flag);
+    landed();
     const uint32_t kt = ring + slot * SL::kItem + k_lane;
     float s[2][NB][4];
     float xc[4];  // factors of the scores of keys gr + 8 i
@@ -752,7 +778,7 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
     release();
     if (odd) load_v();
     else load_k();
-    ok &= mbar_wait(full + 8u * slot, phase, abort_flag);  // V, and its scales
+    landed();  // V, and its scales
 
     // ---- weights
     const uint32_t vt = ring + slot * SL::kItem;
