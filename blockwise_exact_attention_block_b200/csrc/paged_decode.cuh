@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
   const uint32_t v_lane = ET == kCacheBf16 ? pg_off<ROW>((lane & 7) + 8 * (lane >> 4), (lane >> 3) & 1)
                                            : pg_off<ROW>(lane & 15, 0);
   while (true) {
-    if (!__all_sync(0xffffffffu, ok)) break;
+    if (TEAMS && !__all_sync(0xffffffffu, ok)) break;  // (a warp on its own has looked when it loaded)
     if (lstop && cq == lq) break;  // every loaded tile is done
     const int4 t0 = reinterpret_cast<const int4*>(&queue[cq])[0], t1 = reinterpret_cast<const int4*>(&queue[cq])[1];
     const PgTile tile = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
