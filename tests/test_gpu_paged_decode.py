@@ -541,3 +541,67 @@ def test_zero_values_of_a_long_cache(cuda_lib, dtype):
     tol = (D + 4) * 2.0 ** -24 * float(x.abs().max()) + n * 2.0 ** -24 + 2.0 ** -20 * want
     assert abs(float(lse) - want) <= tol
     assert ra.ra_get_device_status() == ra.RA_OK
+
+
+def test_calls_behind_copies_and_other_streams(cuda_lib):
+    """A step whose lengths and rows come by copies, a fill and another stream's kernel
+    right before it, eager and captured: the calls see what precedes them."""
+    ra = cuda_lib
+    B, Hkv, Hq, D, ps, width = 4, 2, 8, 128, 16, 40
+    gen = torch.Generator().manual_seed(21)
+    table = torch.randperm(B * width, generator=gen).view(B, width).int().cuda()
+    kp, vp = (torch.zeros((B * width, Hkv, ps, D), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    q = torch.randn((B, 1, Hq, D), generator=gen).to(torch.bfloat16).cuda()
+    lens, out, lse = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.empty_like(q), torch.empty((B, 1, Hq), device="cuda")
+    k, v = (torch.empty((B, 1, Hkv, D), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    ws = torch.empty(ra.ra_paged_decode_workspace(B, 1, Hq, Hkv, D), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    host_len = torch.zeros(B, dtype=torch.int32).pin_memory()
+    src = torch.empty((2, B, 1, Hkv, D), dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        lens.copy_(host_len, non_blocking=True)   # a copy from the host
+        k.copy_(src[0])                           # a copy on the device
+        out.zero_()
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            torch.mul(src[1], 1.0, out=v)         # a kernel of another stream
+        here.wait_stream(side)
+        ra.ra_cache_append(k, v, kp, vp, table, lens)
+        ra.ra_paged_decode_attention(q, kp, vp, table, lens, out=out, lse=lse, workspace=ws)
+
+    def run(go):
+        kp.zero_()
+        vp.zero_()
+        gen.manual_seed(22)
+        got = []
+        for i in range(1, 60):
+            torch.cuda.synchronize()
+            host_len.copy_(torch.tensor([i, 2 * i, 3 * i, 7 * i if 7 * i <= width * ps else width * ps]).int())
+            src.copy_(torch.randn(src.shape, generator=gen).to(torch.bfloat16))
+            go()
+            got.append((out.clone(), lse.clone()))
+        torch.cuda.synchronize()
+        return got
+
+    want = run(lambda: (torch.cuda.synchronize(), step(), torch.cuda.synchronize()))
+    eager = run(step)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        step()
+    torch.cuda.current_stream().wait_stream(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    replayed = run(graph.replay)
+    for got in (eager, replayed):
+        for (a, b), (c, d) in zip(got, want):
+            assert torch.equal(a, c) and torch.equal(b, d)
+    # the last step against the formula
+    rk, rv = ra.ra_cache_read(kp, vp, table, lens, int(lens.max()), out_dtype=torch.float32)
+    n = int(lens[3])
+    x = torch.einsum("hd,td->ht", q[3, 0, :4].double(), rk[3, :n, 0].double()) / math.sqrt(D)
+    assert torch.allclose(torch.logsumexp(x, 1), lse[3, 0, :4].double(), atol=1e-4)
+    assert ra.ra_get_device_status() == ra.RA_OK
