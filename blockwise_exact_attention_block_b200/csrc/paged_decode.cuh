@@ -59,7 +59,6 @@
 
 #include <type_traits>
 
-#include "attn_fwd.cuh"
 #include "decode.cuh"
 #include "paged.cuh"
 
@@ -114,7 +113,7 @@ struct PgSmem {
   static constexpr int kRow = D * kElem;  // bytes of a cached row
   static constexpr int kScale = kWarps * kRing;                          // fp32 [slots][32]
   static constexpr int kMeta = kScale + (ET == kCacheBf16 ? 0 : kWarps * kSlots * kPgKeys * 4);
-  static constexpr int kFull = kMeta + kWarps * kPgQueue * 32;           // barriers of the ring items
+  static constexpr int kFull = kMeta + kWarps * kPgQueue * 32;           // barriers of a team's ring items
   static constexpr int kEmpty = kFull + kWarps * kSlots * 8;
   static constexpr int kQFull = kEmpty + kWarps * kSlots * 8;            // and of the queue entries
   static constexpr int kQEmpty = kQFull + kWarps * kPgQueue * 8;
