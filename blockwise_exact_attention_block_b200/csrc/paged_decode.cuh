@@ -27,6 +27,13 @@
 // warp whose rows differ by more than 2^16 scales each row by itself and brings
 // the scores to the largest's scale.
 //
+// The tensor core cuts its fp32 sums off instead of rounding them, always towards
+// zero.  So o never goes through it: a tile's products start from zero and are added
+// to o by rounded additions, two to an instruction.  With o as the product's
+// accumulator a run of 50,000 keys came out 3.7e-4 too small, 6e-7 this way.  It
+// costs 5 to 7 % where instruction issue is the bound (8 x 9k-24k int8 keys, 16 rows:
+// 77.5 us then, 82 now), up to 13 % for a bf16 team of several warps, nothing where HBM is.
+//
 // Bound by HBM: a cached element meets the groups * Tq (<= 64) query rows of its
 // KV head and is used once.  So the cache is streamed once, through rings of
 // shared memory, by 16-byte asynchronous copies: a page of one head may be as
@@ -904,21 +911,26 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
       __syncwarp();
     }
     if (!slow) {
+      uint32_t pb[2][3][NB][2];
 #pragma unroll
-      for (int kh = 0; kh < 2; ++kh) {
-        uint32_t pb[3][NB][2];
+      for (int kh = 0; kh < 2; ++kh)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int k8 = 0; k8 < 2; ++k8) {
             uint32_t t[3];
             split_pair<ET>(w[kh][nb][2 * k8], w[kh][nb][2 * k8 + 1], !a.out_bf16, t);
-            pb[0][nb][k8] = transpose_8x8(t[0]);
-            pb[1][nb][k8] = transpose_8x8(t[1]);
-            pb[2][nb][k8] = ET == kCacheBf16 && !a.out_bf16 ? transpose_8x8(t[2]) : 0u;
+            pb[kh][0][nb][k8] = transpose_8x8(t[0]);
+            pb[kh][1][nb][k8] = transpose_8x8(t[1]);
+            pb[kh][2][nb][k8] = ET == kCacheBf16 && !a.out_bf16 ? transpose_8x8(t[2]) : 0u;
           }
 #pragma unroll
-        for (int c = 0; c < KS; ++c) {  // 16 output columns
+      for (int c = 0; c < KS; ++c) {  // 16 output columns
+        float part[NB][4];  // the tile's sums
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) part[nb][0] = part[nb][1] = part[nb][2] = part[nb][3] = 0.f;
+#pragma unroll
+        for (int kh = 0; kh < 2; ++kh) {
           uint32_t va[4];
           if constexpr (ET == kCacheBf16) {
             ldsm_x4_t(((vt + v_lane) ^ (32u * c)) + 16 * ROW * kh, va);
@@ -944,11 +956,17 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
 #pragma unroll
           for (int term = 0; term < 2; ++term)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) pg_mma<ET>(o[c][nb], va, pb[term][nb][0], pb[term][nb][1]);
+            for (int nb = 0; nb < NB; ++nb) pg_mma<ET>(part[nb], va, pb[kh][term][nb][0], pb[kh][term][nb][1]);
           if (ET == kCacheBf16 && !a.out_bf16)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) pg_mma<ET>(o[c][nb], va, pb[2][nb][0], pb[2][nb][1]);
+            for (int nb = 0; nb < NB; ++nb) pg_mma<ET>(part[nb], va, pb[kh][2][nb][0], pb[kh][2][nb][1]);
         }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2)
+            f2_unpack(f2_add(f2_pack(o[c][nb][e], o[c][nb][e + 1]), f2_pack(part[nb][e], part[nb][e + 1])), o[c][nb][e],
+                      o[c][nb][e + 1]);
       }
     } else {
       // key by key, each row taking only the keys that it sees
