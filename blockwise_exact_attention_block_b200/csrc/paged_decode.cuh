@@ -12,16 +12,19 @@
 //     l = sum 2^(x_j - E),   o = sum w_j v_j,   out = o / l,   lse = ln 2 (E + log2 l)
 // with k_j, v_j the codes as they are stored.  E is any reference for which no
 // term overflows: out and lse do not depend on it.  It starts at the first
-// tile's max (x_j + log2 vs_j), which makes the largest w_j 1, and is raised, with
-// l and o rescaled, only when a w_j passes kPgLazy.  So most tiles need no
-// maximum across lanes at all: each lane looks at its own terms, and one vote
-// says that none is too large.
+// tile's max (x_j + log2 vs_j) less kPgStart, which makes the largest w_j 2^kPgStart, and is
+// raised to that of a later tile, with l and o rescaled, only when a w_j passes kPgLazy.
+// So most tiles need no maximum across lanes at all: each lane looks at its own
+// terms, and one vote says that none is too large.
 //
 // The weights w_j go to the tensor core as two 16-bit terms, the leading bits
 // and the rounded remainder, or three for an fp32 output: with bf16 (cache in
-// bf16) 2^-17 or 2^-24 relative, with f16 (8-bit cache) 2^-22 relative and
-// 2^-25 of the largest w.  One rounded term (2^-9 for bf16) would cost as much
-// accuracy as the output's own rounding.  8-bit codes are turned into f16, which
+// bf16) 2^-16 or 2^-24 relative, with f16 (8-bit cache) 2^-22 relative and
+// 2^-24 / 2^kPgStart of the row's largest w.  (At kPgStart = 0 a run of 50,000 keys 2^-25
+// below the largest was missing from o, 1.4e-3 of it, while l had them; at 12, eight times
+// below kPgLazy, the reference moves often: 8 x 9k-24k int8 keys, 16 rows 83 us, at 5 to 10
+// 81.5.)  One rounded term (2^-8 for bf16) would cost as much accuracy as the output's
+// own rounding.  8-bit codes are turned into f16, which
 // holds them exactly; the queries then go in as f16 too, scaled by a power of two
 // that brings the warp's largest to 2^14 (bf16's 8 bits fit down to 2^-30 of it).  A
 // warp whose rows differ by more than 2^16 scales each row by itself and brings
@@ -75,7 +78,12 @@ constexpr int kPgKeys = 32;         // keys of a tile
 constexpr int kPgQueue = 8;         // tiles queued for a team
 constexpr int kPgSlots = 8;         // ring items per warp, at most
 constexpr int kPgPairCost = 3;      // a pair's start and end, in tiles
-constexpr float kPgLazy = 1024.f;   // a weight above this moves the reference E (f16 ends at 65504)
+// log2 of the largest weight when the reference E is set, and the weight above which
+// E moves.  bf16 terms have fp32's range; f16 ones end at 65504 and at 2^-24.
+template <int ET>
+constexpr float kPgStart = ET == kCacheBf16 ? 0.f : 10.f;
+template <int ET>
+constexpr float kPgLazy = ET == kCacheBf16 ? 1024.f : 32768.f;
 constexpr int kPgNone = 0x7fffff00; // position of a key that no row sees
 
 struct PagedArgs {
@@ -837,7 +845,7 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
     if (!raise) {
       if (masked) weigh(std::true_type{});
       else weigh(std::false_type{});
-      raise = __any_sync(0xffffffffu, top > kPgLazy);
+      raise = __any_sync(0xffffffffu, top > kPgLazy<ET>);
     }
     if (raise) {
 #pragma unroll
@@ -850,12 +858,12 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
             const int e = 2 * k8 + (i & 1);
             float x = s[mb][i >> 1][e] * xc[2 * mb + k8];
             // (a scale below those that an append writes could make l overflow)
-            if constexpr (ET != kCacheBf16) x += fmaxf(__log2f(vs[2 * mb + k8]), -100.f);
+            if constexpr (ET != kCacheBf16) x += fmaxf(__log2f(vs[2 * mb + k8]), kPgStart<ET> - 100.f);
             if ((seen >> (8 * mb + 4 * (i >> 1) + e)) & 1u) y = fmaxf(y, x);
           }
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, x));
-        const float En = fmaxf(E[i], y);
+        const float En = fmaxf(E[i], y - kPgStart<ET>);
         const float al = E[i] == -INFINITY ? 0.f : fast_exp2(E[i] - En);
         E[i] = En;
         l[i] *= al;

@@ -67,3 +67,34 @@ def test_sums_of_a_long_run_do_not_drift(cuda_lib, dtype, rows):
     exact = torch.logsumexp(x, 0)
     assert (lse.double() - exact).abs().max() <= sums + 2.0 ** -21 + 2.0 ** -23 * exact
     assert ra.ra_get_device_status() == ra.RA_OK
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [1, 12, 20])
+def test_a_long_tail_of_small_weights_counts(cuda_lib, dtype, rows):
+    """One key, and 49,999 whose weights are 2^-25.15 of its own: 1.4e-3 of the result.  Each
+    weight of an 8-bit cache is held to 2^-34 of the largest; its exponent of 25.15 (the
+    score in binary units) to 2^-22 of itself and the exponential to 2^-21; a run's 1,563 tiles are
+    added with one rounding each, in o and in l, where the first key's lane rounds at its 1."""
+    ra = cuda_lib
+    n, D = 50000, 64
+    k, v = torch.zeros((n, D)), torch.ones((n, D))
+    k[1:, 0], k[:, 1] = -1.0, 1.0
+    v[0] = 0.0
+    v[0, 5] = 1.0
+    c = Shared(ra, dtype, k, v, MANY)
+    q = torch.zeros((MANY, 1, rows, D), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 25.15 * math.log(2) * math.sqrt(D)
+    out, lse = c.decode(ra, q, out_dtype=torch.float32)
+    x = c.k @ q[0, 0, 0].double() / math.sqrt(D)
+    want = torch.softmax(x, 0) @ c.v
+    tail = want[0].item()
+    assert 1e-3 < tail < 2e-3
+    sums, each = 1563 * 2.0 ** -24, 25.5 * 2.0 ** -22 + 2.0 ** -21
+    off = (out.double() - want).abs()
+    only_tail = torch.arange(D, device="cuda") != 5
+    tol = n * 2.0 ** -34 + tail * (2 * sums + each + 2.0 ** -22)
+    assert off[..., only_tail].max() <= tol, f"off by {off[..., only_tail].max():.3g} where {tol:.3g} may be"
+    assert off[..., 5].max() <= n * 2.0 ** -34 + 2 * sums + tail * each + 2.0 ** -21
+    assert (lse.double() - torch.logsumexp(x, 0)).abs().max() <= sums + tail * each + 2.0 ** -22
+    assert ra.ra_get_device_status() == ra.RA_OK
