@@ -629,6 +629,7 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
   float o[KS][NB][4], E[NR], l[NR], qscale = a.scale_log2;
   float rowscale[NR];  // (8-bit cache, `uneven`) this lane's rows' scales by the warp's
   bool uneven = false;
+  bool unset = false;  // the warp has a real row without a reference: all its scores so far are -inf
   int lim[NR], minlim = 0;
   // lane parts of the shared-memory addresses; a chunk index goes in by exclusive or
   // (the slots begin at multiples of the 256 bytes that it can change)
@@ -831,7 +832,9 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const bool hide = kMask && !((seen >> (8 * mb + 4 * nb + e)) & 1u);
-            float p = fast_exp2(fmaf(s[mb][nb][e], xc[2 * mb + (e >> 1)], -E[2 * nb + (e & 1)]));
+            // (without a reference 2^x stands for 2^(x - E): 0, as -inf is all that a row can have there, or NaN)
+            const float ref = E[2 * nb + (e & 1)], r0 = kMask && ref == -INFINITY ? 0.f : ref;
+            float p = fast_exp2(fmaf(s[mb][nb][e], xc[2 * mb + (e >> 1)], -r0));
             if (hide) p = 0.f;
             lt[2 * nb + (e & 1)] += p;
             if constexpr (ET != kCacheBf16) p *= vs[2 * mb + (e >> 1)];
@@ -841,13 +844,14 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
           top = fmax3(fmax3(top, w[mb][nb][0], w[mb][nb][1]), w[mb][nb][2], w[mb][nb][3]);
         }
     };
-    bool raise = flags & kPgFirst;  // (E = -inf there)
+    bool raise = (flags & kPgFirst) || unset;  // (E = -inf there)
     if (!raise) {
       if (masked) weigh(std::true_type{});
       else weigh(std::false_type{});
       raise = __any_sync(0xffffffffu, top > kPgLazy<ET>);
     }
     if (raise) {
+      unset = false;
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
         float y = -INFINITY;  // largest x_j + log2 vs_j of the row's visible keys
@@ -866,6 +870,7 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
         const float En = fmaxf(E[i], y - kPgStart<ET>);
         const float al = E[i] == -INFINITY ? 0.f : fast_exp2(E[i] - En);
         E[i] = En;
+        unset |= lim[i] > 0 && En == -INFINITY;
         l[i] *= al;
 #pragma unroll
         for (int c = 0; c < KS; ++c) {
@@ -873,6 +878,7 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
           o[c][i >> 1][2 + (i & 1)] *= al;
         }
       }
+      unset = __any_sync(0xffffffffu, unset);
       weigh(std::true_type{});
     }
 #pragma unroll

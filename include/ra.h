@@ -403,8 +403,12 @@ ra_status ra_cache_read(const ra_paged_cache* cache, int first, int T, void* k, 
  *             counts as -1.
  *  out, lse   device, out_dtype (RA_F32 or RA_BF16, nearest even) [B, Tq, Hq, D]
  *             and fp32 [B, Tq, Hq], every row written.  A row that is not
- *             real or sees no key gets out = 0, lse = -inf.  What masked places
- *             hold (NaN, infinities, memory never written) has no effect.
+ *             real or sees no key gets out = 0, lse = -inf, and so does one
+ *             whose scores are all -inf (infinite keys); beside other scores
+ *             one of -inf weighs 0.  What masked places hold (NaN, infinities,
+ *             memory never written) has no effect; a NaN or an infinity among
+ *             the values that a row sees, or a score of NaN or +inf, leaves the
+ *             row's out without a finite value in the columns that it reaches.
  *  workspace  device scratch of ra_paged_decode_workspace() bytes, 256-byte
  *             aligned; its contents need no preparation.  Calls that may run at
  *             the same time need one each.

@@ -98,3 +98,50 @@ def test_a_long_tail_of_small_weights_counts(cuda_lib, dtype, rows):
     assert off[..., 5].max() <= n * 2.0 ** -34 + 2 * sums + tail * each + 2.0 ** -21
     assert (lse.double() - torch.logsumexp(x, 0)).abs().max() <= sums + tail * each + 2.0 ** -22
     assert ra.ra_get_device_status() == ra.RA_OK
+
+
+@pytest.mark.parametrize("n,ps,where", [
+    (33, 16, [32]),                    # the newest key, in a tile of its own
+    (1281, 16, [1280]),                # the same behind other warps' tiles
+    (70, 32, list(range(32))),         # all of the first tile
+    (600, 128, list(range(0, 600, 2))),
+    (900, 64, list(range(800))),       # whole runs of other warps
+])
+@pytest.mark.parametrize("rows", [1, 12, 20])
+@pytest.mark.parametrize("odt", [torch.bfloat16, torch.float32])
+def test_scores_of_minus_infinity_weigh_nothing(cuda_lib, n, ps, where, rows, odt):
+    """Keys with an infinite column that the queries take with the other sign: weight 0,
+    wherever a warp's run begins.  Odd rows have a 0 there (0 times infinity is NaN), and
+    stay apart; a row all of whose keys are such is empty."""
+    ra = cuda_lib
+    D, pages = 64, -(-n // ps)
+    gen = torch.Generator().manual_seed(n)
+    k, v = torch.randn((pages * ps, D), generator=gen), torch.randn((pages * ps, D), generator=gen)
+    k[:, 0] = 0.0
+    k[where, 0] = -math.inf
+    kp, vp = (x.to(torch.bfloat16).view(pages, 1, ps, D).cuda() for x in (k, v))
+    q = torch.randn((1, 1, rows, D), generator=gen)
+    q[..., 0] = 1.0
+    odd = torch.arange(rows) % 2 == 1
+    q[:, :, odd, 0] = 0.0
+    q = q.to(torch.bfloat16)
+    table = torch.arange(pages, dtype=torch.int32)[None].contiguous().cuda()
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    out, lse = ra.ra_paged_decode_attention(q.cuda(), kp, vp, table, lens, out_dtype=odt)
+    kd, vd = k[:n].to(torch.bfloat16).double(), v[:n].to(torch.bfloat16).double()
+    x = q[0, 0, ~odd].double() @ kd.T / math.sqrt(D)
+    assert torch.isneginf(x[:, where]).all()
+    want, l = torch.softmax(x, 1) @ vd, torch.logsumexp(x, 1)
+    # scores to (D + 4) 2^-24 of their terms, weights, exponentials and up to 600 / 8 sums of them, the output's rounding
+    terms = (q[0, 0, ~odd].abs().double()[:, 1:].max() * kd[:, 1:].abs().sum(1).max()).item() / math.sqrt(D)
+    dx = (D + 4) * 2.0 ** -24 * terms + 2.0 ** -21 + 80 * 2.0 ** -24
+    tol = 2 * (dx + 2.0 ** -16) * vd.abs().max() + torch.finfo(odt).eps / 2 * want.abs()
+    got, gl = out[0, 0, ~odd].cpu().double(), lse[0, 0, ~odd].cpu().double()
+    assert (got - want).abs().le(tol).all()
+    assert ((gl - l).abs() <= dx + 2.0 ** -23 * l.abs()).all()
+    assert torch.isnan(out[0, 0, odd]).all()
+    all_inf = torch.full_like(kp, -math.inf)
+    q.fill_(1.0)
+    out, lse = ra.ra_paged_decode_attention(q.cuda(), all_inf, vp, table, lens, out_dtype=odt)
+    assert not out.any() and torch.isneginf(lse).all()
+    assert ra.ra_get_device_status() == ra.RA_OK
