@@ -843,6 +843,11 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
           }
           top = fmax3(fmax3(top, w[mb][nb][0], w[mb][nb][1]), w[mb][nb][2], w[mb][nb][3]);
         }
+      // Values of tiny scales weigh little and count in l in full: its terms move E at
+      // 2^104 too.  (An E just set leaves a lane's four at 2^102 at most, see below.)
+      if constexpr (ET != kCacheBf16)
+#pragma unroll
+        for (int i = 0; i < NR; ++i) top = fmaxf(top, lt[i] * (kPgLazy<ET> * 0x1p-104f));
     };
     bool raise = (flags & kPgFirst) || unset;  // (E = -inf there)
     if (!raise) {
@@ -861,7 +866,7 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
           for (int k8 = 0; k8 < 2; ++k8) {
             const int e = 2 * k8 + (i & 1);
             float x = s[mb][i >> 1][e] * xc[2 * mb + k8];
-            // (a scale below those that an append writes could make l overflow)
+            // (no term of l above 2^100, or l could overflow; an append's scales are 2^-109 or more)
             if constexpr (ET != kCacheBf16) x += fmaxf(__log2f(vs[2 * mb + k8]), kPgStart<ET> - 100.f);
             if ((seen >> (8 * mb + 4 * (i >> 1) + e)) & 1u) y = fmaxf(y, x);
           }

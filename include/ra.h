@@ -414,7 +414,9 @@ ra_status ra_cache_read(const ra_paged_cache* cache, int first, int T, void* k, 
  *             the same time need one each.
  * Sums are held in fp32.  A key's weight in out is held to 2^-16 of itself (bf16
  * cache and output), 2^-24 (bf16 cache, fp32 output) or 2^-22 (8-bit cache); in an
- * 8-bit cache, weight times value scale at least to 2^-34 of the row's largest.
+ * 8-bit cache, weight times value scale at least to 2^-34 of the row's largest (to
+ * 2^-15 where all its value scales lie between 2^-90 and 2^-109, an append's
+ * smallest; scales below that lose out's bits, not lse's).
  * No atomics: the result does not depend on scheduling.  The call reads the
  * lengths on the device; captured in a graph, it replays with those then in place.
  */

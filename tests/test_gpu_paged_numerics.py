@@ -145,3 +145,36 @@ def test_scores_of_minus_infinity_weigh_nothing(cuda_lib, n, ps, where, rows, od
     out, lse = ra.ra_paged_decode_attention(q.cuda(), all_inf, vp, table, lens, out_dtype=odt)
     assert not out.any() and torch.isneginf(lse).all()
     assert ra.ra_get_device_status() == ra.RA_OK
+
+
+@pytest.mark.parametrize("dtype", ["int8", "e4m3"])
+@pytest.mark.parametrize("rows", [1, 12, 20])
+@pytest.mark.parametrize("shift,growth", [(0, 16.9), (-13, 26.0)])
+def test_tiny_values_do_not_overflow_the_sum(cuda_lib, dtype, rows, shift, growth):
+    """Values of 2^-99, the smallest that an append keeps, and scores that grow by 16.9 binary
+    units behind the first tile: 2^17 keys' worth of terms in l beside a first tile that the
+    tiny scales let count 2^100.  Weight times scale is held to 2^-15 of the largest, the
+    score (16.9 units) to 2^-22 of itself, sums as in the test of long runs.  With scales 2^-13
+    smaller yet (no append's) the lse is still asked for."""
+    ra = cuda_lib
+    n, D = 20000, 64
+    gen = torch.Generator().manual_seed(rows)
+    k, v = torch.zeros((n, D)), (0.5 + 0.5 * torch.rand((n, D), generator=gen)) * 2.0 ** -99
+    k[32:, 0], k[:, 1] = 1.0, 1.0
+    v[:, 5] = 2.0 ** -99
+    c = Shared(ra, dtype, k, v, MANY)
+    assert 2.0 ** -109 <= c.scales["v_scales"][c.scales["v_scales"] > 0].min() < 2.0 ** -105
+    c.scales["v_scales"] *= 2.0 ** shift
+    q = torch.zeros((MANY, 1, rows, D), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = growth * math.log(2) * math.sqrt(D)
+    out, lse = c.decode(ra, q, out_dtype=torch.float32)
+    x = c.k @ q[0, 0, 0].double() / math.sqrt(D)
+    each, sums = (growth + 1) * 2.0 ** -22 + 2.0 ** -21, 625 * 2.0 ** -24
+    exact = torch.logsumexp(x, 0)
+    assert (lse.double() - exact).abs().max() <= each + sums + 2.0 ** -23 * exact
+    if shift == 0:
+        want = torch.softmax(x, 0) @ c.v
+        off = ((out.double() - want).abs() / c.v.max()).max().item()
+        tol = 2.0 ** -15 + 2 * (each + sums) + 6 * 2.0 ** -23 + 2.0 ** -22
+        assert off <= tol, f"off by {off:.3g}, {off / tol:.3g} tolerances"
+    assert ra.ra_get_device_status() == ra.RA_OK
