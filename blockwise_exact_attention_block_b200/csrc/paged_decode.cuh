@@ -382,13 +382,16 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
     const int idx = static_cast<int>(key >> a.bt.page_shift);
     if (idx >= min(a.n_sel, pages)) return -1;
     const int* sel = a.selected + (static_cast<long long>(b) * a.bt.Hkv + h) * a.n_sel;
-    const int x = sel[idx], prev = idx > 0 ? sel[idx - 1] : -1;
+    const int x = sel[idx];
+    int prev = idx > 0 ? sel[idx - 1] : -1;  // the entry in range before it: as a rule the last one
     if (x == -1) return -1;
-    if (x < 0 || x >= pages || x <= prev) {
-      set_status(RA_ERR_DEVICE_BOUNDS);
-      return -1;
+    bool good = x >= 0 && x < pages;
+    if (good) {
+      for (int i = idx - 2; (prev < 0 || prev >= pages) && i >= 0; --i) prev = sel[i];
+      good = x > prev || prev >= pages;
     }
-    return x;
+    if (!good) set_status(RA_ERR_DEVICE_BOUNDS);
+    return good ? x : -1;
   };
   // the tile's one or two pages: table indices and what the table holds there
   int lg0 = -1, lg1 = -1, pg0 = 0, pg1 = 0;

@@ -397,10 +397,11 @@ ra_status ra_cache_read(const ra_paged_cache* cache, int first, int T, void* k, 
  *  causal     nonzero: row i sees keys j <= p; else keys j < seq_lens[b].
  *  selected   device int32 [B, Hkv, n_sel], or NULL (n_sel = 0) for the whole
  *             cache: table indices of the pages that each KV head sees, strictly
- *             ascending, -1 for no page.  Of each list the first min(n_sel,
- *             ceil(seq_lens[b] / page_size)) entries are read; one that is out of
- *             range or does not ascend is recorded as RA_ERR_DEVICE_BOUNDS and
- *             counts as -1.
+ *             ascending, -1 for no page (anywhere in a list).  Of each list the
+ *             first min(n_sel, ceil(seq_lens[b] / page_size)) entries are read; one
+ *             that is out of range, or not above the nearest one in range before
+ *             it, is recorded as RA_ERR_DEVICE_BOUNDS and counts as -1.  So of a
+ *             list that does not ascend an entry is always recorded.
  *  out, lse   device, out_dtype (RA_F32 or RA_BF16, nearest even) [B, Tq, Hq, D]
  *             and fp32 [B, Tq, Hq], every row written.  A row that is not
  *             real or sees no key gets out = 0, lse = -inf, and so does one
