@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_
     if (p0 >= count) return;
     const bool bad = lane < 16 && p0 + lane < count && (raw < 0 || raw >= a.bt.n_pages);
     if (bad) set_status(RA_ERR_DEVICE_BOUNDS);
-    const int mine = bad || p0 + lane >= count ? 0 : raw;  // a page without bounds is read as page 0 and not written
+    const int mine = bad || p0 + lane >= count ? -1 : raw;  // (a slot without a page has bounds of 0: nothing counts there)
     const int real = s.fresh * a.groups;                   // rows of real tokens come first
     if (gr >= real)
 #pragma unroll
@@ -103,10 +103,15 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // pages gr and gr + 8
       const int page = __shfl_sync(0xffffffffu, mine, gr + 8 * i);
-      const uint4* src = reinterpret_cast<const uint4*>(a.bounds + (static_cast<long long>(page) * a.bt.Hkv + h) * 2 * D) + qd;
+      const uint4* src =
+          reinterpret_cast<const uint4*>(a.bounds + (static_cast<long long>(max(page, 0)) * a.bt.Hkv + h) * 2 * D) + qd;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const uint4 x = src[4 * j], y = src[D / 8 + 4 * j];
+        uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+        if (page >= 0) {
+          x = src[4 * j];
+          y = src[D / 8 + 4 * j];
+        }
         lo[i][j][0] = x.x, lo[i][j][1] = x.y, lo[i][j][2] = x.z, lo[i][j][3] = x.w;
         hi[i][j][0] = y.x, hi[i][j][1] = y.y, hi[i][j][2] = y.z, hi[i][j][3] = y.w;
       }
