@@ -37,16 +37,23 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 
-def _load_paged():
-    """The extension module that marshals the paged cache's calls."""
-    path = os.path.join(_PKG, "_paged.so")
-    if not os.path.exists(path):
-        raise ImportError(f"{path} is missing: build it with `python blockwise_exact_attention_block_b200/build.py`")
-    name = __name__ + "._paged"
-    loader = importlib.machinery.ExtensionFileLoader(name, path)
-    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader(name, loader))
-    loader.exec_module(mod)
-    return mod
+_paged_module = None
+
+
+def _paged():
+    """The extension module that marshals the paged cache's calls, loaded by the first of them
+    (it needs the torch that it was built with; the rest of the library does not need it)."""
+    global _paged_module
+    if _paged_module is None:
+        path = os.path.join(_PKG, "_paged.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it with `python blockwise_exact_attention_block_b200/build.py`")
+        name = __name__ + "._paged"
+        loader = importlib.machinery.ExtensionFileLoader(name, path)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader(name, loader))
+        loader.exec_module(mod)
+        _paged_module = mod
+    return _paged_module
 
 
 RA_OK, RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_WORKSPACE = 0, 1, 2, 3
@@ -463,7 +470,6 @@ def ra_decode_attention(q, k, v, causal: bool = True, n_splits: int = 0, out=Non
 # a decoding step makes several for every token, and checking a dozen tensors in
 # Python took longer than the kernels.
 
-_paged = _load_paged()
 _fn = {name: ctypes.cast(getattr(_lib, name), _vp).value
        for name in ("ra_cache_append", "ra_cache_read", "ra_paged_decode_attention", "ra_paged_decode_workspace",
                     "ra_page_select", "ra_page_select_workspace")}
@@ -479,8 +485,8 @@ def ra_cache_append(k, v, k_pages, v_pages, page_table, seq_lens, new_lens=None,
     scales of an 8-bit cache and, if given, the pages' key bounds.  seq_lens
     counts the new tokens in; row i < new_lens[b] is the token at position
     seq_lens[b] - new_lens[b] + i (None: min(T, seq_lens[b]) of them)."""
-    status = _paged.append(_fn["ra_cache_append"], k, v, k_pages, v_pages, page_table, seq_lens, new_lens, k_scales,
-                           v_scales, key_bounds, _handle(stream))
+    status = _paged().append(_fn["ra_cache_append"], k, v, k_pages, v_pages, page_table, seq_lens, new_lens, k_scales,
+                             v_scales, key_bounds, _handle(stream))
     if status != RA_OK:
         raise RAError(status, "ra_cache_append")
 
@@ -490,8 +496,8 @@ def ra_cache_read(k_pages, v_pages, page_table, seq_lens, T: int, first: int = 0
     """Tokens first .. first + T - 1 of every sequence as dense (k, v)
     [B, T, Hkv, D], zero at and behind seq_lens[b]; out_dtype bfloat16 (default)
     or float32."""
-    status, k, v = _paged.read(_fn["ra_cache_read"], k_pages, v_pages, page_table, seq_lens, T, first, k_scales, v_scales,
-                               k, v, out_dtype, _handle(stream))
+    status, k, v = _paged().read(_fn["ra_cache_read"], k_pages, v_pages, page_table, seq_lens, T, first, k_scales,
+                                 v_scales, k, v, out_dtype, _handle(stream))
     if status != RA_OK:
         raise RAError(status, "ra_cache_read")
     return k, v
@@ -512,9 +518,9 @@ def ra_paged_decode_attention(q, k_pages, v_pages, page_table, seq_lens, new_len
     gives them).  Row i < new_lens[b] is the token at position seq_lens[b] -
     new_lens[b] + i (None: min(Tq, seq_lens[b]) real rows).  Returns
     (out [B, Tq, Hq, D] in out_dtype, default float32; lse [B, Tq, Hq] float32)."""
-    status, out, lse = _paged.decode(_fn["ra_paged_decode_attention"], _fn["ra_paged_decode_workspace"], q, k_pages,
-                                     v_pages, page_table, seq_lens, new_lens, k_scales, v_scales, causal, selected, out,
-                                     lse, out_dtype, workspace, _handle(stream))
+    status, out, lse = _paged().decode(_fn["ra_paged_decode_attention"], _fn["ra_paged_decode_workspace"], q, k_pages,
+                                       v_pages, page_table, seq_lens, new_lens, k_scales, v_scales, causal, selected,
+                                       out, lse, out_dtype, workspace, _handle(stream))
     if status != RA_OK:
         raise RAError(status, "ra_paged_decode_attention")
     return out, lse
@@ -533,8 +539,8 @@ def ra_page_select(q, key_bounds, page_table, seq_lens, n_sel: int, page_size: i
     queries q [B, Tq, Hq, D] (bf16) by the bound that key_bounds
     [n_pages, Hkv, 2, D] puts on a page's scores: int32 [B, Hkv, n_sel],
     ascending, -1 behind.  The new tokens' own pages are always among them."""
-    status, selected = _paged.select(_fn["ra_page_select"], _fn["ra_page_select_workspace"], q, key_bounds, page_table,
-                                     seq_lens, n_sel, page_size, new_lens, selected, workspace, _handle(stream))
+    status, selected = _paged().select(_fn["ra_page_select"], _fn["ra_page_select_workspace"], q, key_bounds, page_table,
+                                       seq_lens, n_sel, page_size, new_lens, selected, workspace, _handle(stream))
     if status != RA_OK:
         raise RAError(status, "ra_page_select")
     return selected
