@@ -7,7 +7,8 @@
 csrc/api.cu is the main translation unit (it includes every kernel);
 csrc/noalloc.cu adds the entry point whose scratch is a fixed device array.
 csrc/paged_binding.cpp is the CPython extension _paged that marshals the paged
-cache's calls (compiled with the C++ compiler against torch's headers).
+cache's calls (compiled with the C++ compiler against torch's headers; either
+build makes it, and another torch or Python has it made anew).
 --debug-bounds builds the checked variant libra_b200_debug.so instead
 (-DRA_DEBUG_BOUNDS: every run-time-indexed global access is checked; the
 binding loads it when RA_DEBUG_BOUNDS=1 is set in the environment).
@@ -48,10 +49,26 @@ def up_to_date(out: str = OUT) -> bool:
     return all(os.path.getmtime(s) <= t for s in sources())
 
 
+def binding_tag() -> str:
+    """The torch and the Python that the extension module is compiled against; it holds this text,
+    and serves no others (it links torch's C++ symbols)."""
+    import importlib.metadata
+    return f"ra_paged_binding torch {importlib.metadata.version('torch')} {sys.implementation.cache_tag}"
+
+
+def binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING):
+        return False
+    t = os.path.getmtime(BINDING)
+    if not all(os.path.getmtime(s) <= t for s in (BINDING_SRC, os.path.join(ROOT, "include", "ra.h"))):
+        return False
+    with open(BINDING, "rb") as f:
+        return binding_tag().encode() + b"\0" in f.read()
+
+
 def build_binding(force: bool = False) -> str:
     """The extension module of the paged cache's calls (host code only)."""
-    srcs = [BINDING_SRC, os.path.join(ROOT, "include", "ra.h")]
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(s) <= os.path.getmtime(BINDING) for s in srcs):
+    if not force and binding_up_to_date():
         return BINDING
     import sysconfig
 
@@ -63,6 +80,7 @@ def build_binding(force: bool = False) -> str:
            sysconfig.get_paths()["include"]]
     cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DRA_BINDING_TAG="{binding_tag()}"',
            *[f"-I{d}" for d in inc[:1]], *[f"-isystem{d}" for d in inc[1:]], BINDING_SRC, "-o", BINDING + ".tmp",
            "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -73,8 +91,7 @@ def build_binding(force: bool = False) -> str:
 
 
 def build(force: bool = False, ptxas_verbose: bool = False, debug_bounds: bool = False) -> str:
-    if not debug_bounds:
-        build_binding(force)
+    build_binding(force)  # (both libraries' callers load it)
     out = OUT_DEBUG if debug_bounds else OUT
     if not force and up_to_date(out):
         return out

@@ -364,4 +364,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged", "Calls of the paged key-v
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__paged(void) { return PyModule_Create(&module); }
+// What the module was compiled against (build.py looks for it, and compiles it anew for another).
+const char built_for[] = RA_BINDING_TAG;
+
+PyMODINIT_FUNC PyInit__paged(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", built_for) < 0) Py_CLEAR(m);
+  return m;
+}

@@ -56,3 +56,67 @@ def test_older_calls_do_not_need_the_module(tmp_path, module):
     res = subprocess.run([sys.executable, "-c", USE, str(where)], cwd=where, capture_output=True, text=True,
                          env=dict(os.environ, PYTHONPATH=str(where)))
     assert res.returncode == 0 and "done" in res.stdout, res.stdout + res.stderr
+
+
+def build_module(where):
+    """build.py as it is, for a tree of its own in `where`."""
+    import importlib.util
+    pkg = where / NAME
+    pkg.mkdir()
+    for d, to in (("csrc", pkg), ):
+        os.symlink(os.path.join(ROOT, NAME, d), to / d)
+    os.symlink(os.path.join(ROOT, "include"), where / "include")
+    path = pkg / "build.py"
+    path.write_bytes(open(os.path.join(ROOT, NAME, "build.py"), "rb").read())
+    spec = importlib.util.spec_from_file_location("a_build", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+class Compilers:
+    """Stands in for subprocess.run: notes what would be compiled and writes its output."""
+
+    def __init__(self, monkeypatch, mod, text=b""):
+        self.made = []
+        monkeypatch.setattr(mod.subprocess, "run", self.run)
+        self.text = text
+
+    def run(self, cmd, **_):
+        out = cmd[cmd.index("-o") + 1]
+        tags = [x[len("-DRA_BINDING_TAG="):].strip('"').encode() + b"\0" for x in cmd if x.startswith("-DRA_BINDING_TAG=")]
+        with open(out, "wb") as f:
+            f.write(b"".join(tags))
+        self.made.append(os.path.basename(out).removesuffix(".tmp"))
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+
+def test_the_checked_build_makes_the_module_too(tmp_path, monkeypatch):
+    mod = build_module(tmp_path)
+    c = Compilers(monkeypatch, mod)
+    mod.build(debug_bounds=True)
+    assert sorted(c.made) == ["_paged.so", "libra_b200_debug.so"]
+    mod.build(debug_bounds=True)
+    mod.build()
+    assert sorted(c.made) == ["_paged.so", "libra_b200.so", "libra_b200_debug.so"]
+
+
+def test_another_torch_or_python_has_the_module_made_anew(tmp_path, monkeypatch):
+    import importlib.metadata
+    mod = build_module(tmp_path)
+    c = Compilers(monkeypatch, mod)
+    mod.build_binding()
+    mod.build_binding()
+    assert c.made == ["_paged.so"]
+    version = importlib.metadata.version("torch")
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: version + ".1")
+    mod.build_binding()
+    mod.build_binding()
+    assert c.made == ["_paged.so"] * 2
+
+
+def test_the_module_names_what_it_was_built_for():
+    import __graft_entry__
+    import blockwise_exact_attention_block_b200 as ra
+    assert ra._paged().built_for == __graft_entry__._build_module().binding_tag()
+    assert torch.__version__ in ra._paged().built_for
