@@ -99,10 +99,12 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_
     if (gr >= real)
 #pragma unroll
       for (int j = 0; j < J; ++j) q0[j] = make_uint4(0u, 0u, 0u, 0u);  // (padding may hold anything)
+    if (!RA_IN_BOUNDS(b, a.bt.B) || !RA_IN_BOUNDS(p0 + 15, a.stride)) return;
     uint32_t lo[2][J][4], hi[2][J][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // pages gr and gr + 8
-      const int page = __shfl_sync(0xffffffffu, mine, gr + 8 * i);
+      int page = __shfl_sync(0xffffffffu, mine, gr + 8 * i);
+      if (page >= 0 && !RA_IN_BOUNDS(page + PG_INJECTED(a.bt), a.bt.n_pages)) page = -1;
       const uint4* src =
           reinterpret_cast<const uint4*>(a.bounds + (static_cast<long long>(max(page, 0)) * a.bt.Hkv + h) * 2 * D) + qd;
 #pragma unroll
@@ -210,6 +212,7 @@ __device__ __forceinline__ double bound_times(double q, float x) {
 // each; every lane of the warp calls it, with the same number of rows.
 template <int D>
 __device__ __forceinline__ unsigned long long exact_key(const SelectArgs& a, int b, int h, int page, int real, int lr) {
+  if (!RA_IN_BOUNDS(page, a.bt.n_pages)) page = 0;
   const __nv_bfloat16* bl = a.bounds + (static_cast<long long>(page) * a.bt.Hkv + h) * 2 * D + 8 * lr;
   float lo[8], hi[8];
   bf16_octet(bl, lo);
@@ -540,7 +543,7 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
       const int p = min(i + sub, n - 1);
       const int page = page_of(a.bt, b, p);
       const unsigned long long k = exact_key<D>(a, b, h, max(page, 0), real, lr);
-      if (lr == 0 && i + sub < n) slots[p] = page < 0 ? 0ull : k;
+      if (lr == 0 && i + sub < n && RA_IN_BOUNDS(p, a.stride)) slots[p] = page < 0 ? 0ull : k;
     }
     N = n;
     __syncthreads();
@@ -553,13 +556,13 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
     const int ties = want - above;  // of the pages whose key is T, the first in page order
     in_order([&](int i) { return slots[i] > T ? 1 : slots[i] == T ? 2 : 0; },
              [&](int kind, int i, int ones, int twos) {
-               if (kind == 1 || twos < ties) out[ones + min(twos, ties)] = i;
+               if ((kind == 1 || twos < ties) && RA_IN_BOUNDS(ones + min(twos, ties), want)) out[ones + min(twos, ties)] = i;
              });
     return;
   }
   if (close > need) {
     in_order(kind_of, [&](int kind, int i, int, int twos) {
-      if (kind == 2) sh.close_at[twos] = page_at(i);
+      if (kind == 2 && RA_IN_BOUNDS(twos, kSelClose)) sh.close_at[twos] = page_at(i);
     });
     for (int j0 = warp * G; j0 < close; j0 += (kSelThreads / 32) * G) {
       const int j = min(j0 + sub, close - 1);
@@ -598,7 +601,7 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
       if (kind == 2 && x < 0) return;
       before = x < 0 ? -1 - x : x;
     }
-    out[ones + before] = page_at(i);
+    if (RA_IN_BOUNDS(ones + before, want)) out[ones + before] = page_at(i);
   });
 }
 

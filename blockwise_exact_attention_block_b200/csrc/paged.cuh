@@ -31,7 +31,21 @@ struct PagedBatch {
   const int* new_lens;    // [B] or null
   int B, T, max_pages, n_pages, Hkv;
   int page_shift;  // log2(page_size)
+#ifdef RA_DEBUG_BOUNDS
+  long long inject;  // added to an index where it is checked, not where it is used (a test's)
+#endif
 };
+#ifdef RA_DEBUG_BOUNDS
+#define PG_INJECTED(bt) ((bt).inject)
+#else
+#define PG_INJECTED(bt) 0
+#endif
+
+// Extents of the arrays, for the checked build: table entries, cached rows of all heads.
+__device__ __forceinline__ long long table_extent(const PagedBatch& a) { return static_cast<long long>(a.B) * a.max_pages; }
+__device__ __forceinline__ long long row_extent(const PagedBatch& a) {
+  return (static_cast<long long>(a.n_pages) * a.Hkv) << a.page_shift;
+}
 
 // Tokens of sequence b and how many of its T rows are real, held to their ranges.
 struct SeqLen {
@@ -40,6 +54,7 @@ struct SeqLen {
 
 __device__ __forceinline__ SeqLen seq_len_of(const PagedBatch& a, int b) {
   SeqLen s;
+  if (!RA_IN_BOUNDS(b, a.B)) return {0, 0};
   s.len = a.seq_lens[b];
   const int given = a.new_lens ? a.new_lens[b] : 0;  // (both loads before the first check)
   const int cap = a.max_pages << a.page_shift;
@@ -59,7 +74,9 @@ __device__ __forceinline__ SeqLen seq_len_of(const PagedBatch& a, int b) {
 // Page `logical` (below the sequence's page count) of sequence b; -1, recorded,
 // when the table holds no valid page there.
 __device__ __forceinline__ int page_of(const PagedBatch& a, int b, int logical) {
-  const int p = a.page_table[static_cast<long long>(b) * a.max_pages + logical];
+  const long long at = static_cast<long long>(b) * a.max_pages + logical;
+  if (!RA_IN_BOUNDS(logical, a.max_pages) || !RA_IN_BOUNDS(at, table_extent(a))) return -1;
+  const int p = a.page_table[at];
   if (p >= 0 && p < a.n_pages) return p;
   set_status(RA_ERR_DEVICE_BOUNDS);
   return -1;
@@ -265,7 +282,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(const _
     const long long first = static_cast<long long>(logical) << a.bt.page_shift;  // position of the page's row 0
     if (s.fresh > 0 && first < s.len) {
       // (not looked at before the first rows are on their way: the loads overlap)
-      page = a.bt.page_table[static_cast<long long>(b) * a.bt.max_pages + logical];
+      if (RA_IN_BOUNDS(logical, a.bt.max_pages)) page = a.bt.page_table[static_cast<long long>(b) * a.bt.max_pages + logical];
       r0 = max(begin - static_cast<int>(first), 0);
       r1 = min(s.len - static_cast<int>(first), ps);
       tok0 = static_cast<int>(first) - begin;  // token of the page's row 0 (may be negative)
@@ -282,7 +299,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(const _
       for (int u = 0; u < kAppendBatch; ++u) {
         const int r = rb + u * step + sub;
         kw[u] = vw[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < r1) {
+        if (r < r1 && RA_IN_BOUNDS(tok0 + r, a.bt.T) && RA_IN_BOUNDS(b, a.bt.B)) {
           const long long src = ((static_cast<long long>(b) * a.bt.T + tok0 + r) * a.bt.Hkv + h) * D + 8 * lr;
           kw[u] = __ldcs(reinterpret_cast<const uint4*>(a.k + src));
           vw[u] = __ldcs(reinterpret_cast<const uint4*>(a.v + src));
@@ -294,7 +311,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(const _
       for (int u = 0; u < kAppendBatch; ++u) {
         if (rb + u * step >= r1) break;  // the same for the whole warp
         const int r = rb + u * step + sub;
-        const bool act = r < r1 && good;
+        const bool act = r < r1 && good && RA_IN_BOUNDS(prow + r + PG_INJECTED(a.bt), row_extent(a.bt));
         append_row<D, ET>(kw[u], act, lr, a.k_pages, a.k_scales, prow + r);
         append_row<D, ET>(vw[u], act, lr, a.v_pages, a.v_scales, prow + r);
         if (a.bounds && act) {
@@ -334,6 +351,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(const _
         }
   }
   if (!good || wi != 0 || sub != 0) return;
+  if (!RA_IN_BOUNDS(static_cast<long long>(page) * a.bt.Hkv + h, static_cast<long long>(a.bt.n_pages) * a.bt.Hkv)) return;
   uint4* bl = reinterpret_cast<uint4*>(a.bounds + (static_cast<long long>(page) * a.bt.Hkv + h) * 2 * D) + lr;
   if (r0 > 0) {  // earlier tokens' bounds stand in the page
     const uint4 x = bl[0], y = bl[D / 8];
@@ -432,7 +450,8 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_c
   // table entry is loaded beside the length that says whether it counts.
   const long long pos = static_cast<long long>(a.first) + t0 + (lane & (kRows - 1));
   const long long logical = min(pos >> a.bt.page_shift, static_cast<long long>(a.bt.max_pages - 1));
-  const int page = a.bt.page_table[static_cast<long long>(b) * a.bt.max_pages + logical];
+  const long long entry = static_cast<long long>(b) * a.bt.max_pages + logical;
+  const int page = RA_IN_BOUNDS(entry, table_extent(a.bt)) ? a.bt.page_table[entry] : -1;
   const int len = seq_len_of(a.bt, b).len;
   long long mine = -1;
   if (lane < kRows && pos < len) {
@@ -440,6 +459,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_c
       mine = ((static_cast<long long>(page) * a.bt.Hkv + h) << a.bt.page_shift) + (pos & ((1 << a.bt.page_shift) - 1));
     else
       set_status(RA_ERR_DEVICE_BOUNDS);
+    if (mine >= 0 && !RA_IN_BOUNDS(mine + PG_INJECTED(a.bt), row_extent(a.bt))) mine = -1;
   }
   Octet<ET> o[2][N];
 #pragma unroll
@@ -455,7 +475,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int t = t0 + i * RPW + sub;
-      if (t >= a.bt.T) continue;
+      if (t >= a.bt.T || !RA_IN_BOUNDS(b, a.bt.B)) continue;
       Tout* dst = static_cast<Tout*>(a.out[kv]) + ((static_cast<long long>(b) * a.bt.T + t) * a.bt.Hkv + h) * D + 8 * lr;
       if constexpr (sizeof(Tout) == 2 && ET == kCacheBf16) {
         __stcs(reinterpret_cast<uint4*>(dst), o[kv][i].w);

@@ -2,6 +2,8 @@
 // argument validation and launches.  Included by api.cu, whose helpers it uses.
 #pragma once
 
+#include <stdlib.h>
+
 #include "page_select.cuh"
 #include "paged.cuh"
 #include "paged_decode.cuh"
@@ -54,6 +56,11 @@ PagedBatch batch_of(const ra_paged_cache* c, int T) {
   b.n_pages = c->n_pages;
   b.Hkv = c->Hkv;
   b.page_shift = page_shift_of(c->page_size);
+#ifdef RA_DEBUG_BOUNDS
+  // an offset that one check of each kernel adds to its index: the check fails, the access is left out
+  const char* inject = getenv("RA_DEBUG_INJECT_PAGED");
+  b.inject = inject ? atoll(inject) : 0;
+#endif
   return b;
 }
 

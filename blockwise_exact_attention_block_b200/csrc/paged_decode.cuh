@@ -381,6 +381,7 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
     const int pages = (s.len + ps - 1) >> a.bt.page_shift;
     const int idx = static_cast<int>(key >> a.bt.page_shift);
     if (idx >= min(a.n_sel, pages)) return -1;
+    if (!RA_IN_BOUNDS(b, a.bt.B) || !RA_IN_BOUNDS(h, a.bt.Hkv) || !RA_IN_BOUNDS(idx, a.n_sel)) return -1;
     const int* sel = a.selected + (static_cast<long long>(b) * a.bt.Hkv + h) * a.n_sel;
     const int x = sel[idx];
     int prev = idx > 0 ? sel[idx - 1] : -1;  // the entry in range before it: as a rule the last one
@@ -398,9 +399,11 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
   auto look_up = [&]() {
     const int* row = a.bt.page_table + static_cast<long long>(b) * a.bt.max_pages;
     lg0 = logical_of(2 * t);
+    if (!RA_IN_BOUNDS(b, a.bt.B) || (lg0 >= 0 && !RA_IN_BOUNDS(lg0, a.bt.max_pages))) lg0 = -1;
     if (lg0 >= 0) pg0 = row[lg0];
     if (ps == 16) {
       lg1 = logical_of(2 * t + 1);
+      if (!RA_IN_BOUNDS(b, a.bt.B) || (lg1 >= 0 && !RA_IN_BOUNDS(lg1, a.bt.max_pages))) lg1 = -1;
       if (lg1 >= 0) pg1 = row[lg1];
     }
   };
@@ -428,6 +431,11 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
             set_status(RA_ERR_DEVICE_BOUNDS);
             return;
           }
+          // (the consumers copy 16 rows from r, or 32 of a page that holds as many)
+          if (!RA_IN_BOUNDS((((static_cast<long long>(pg) * a.bt.Hkv + h) << a.bt.page_shift) + (key & (ps - 1))) +
+                                min(ps, kPgKeys) - 1 + PG_INJECTED(a.bt),
+                            row_extent(a.bt)))
+            return;
           r = ((pg * a.bt.Hkv + h) << a.bt.page_shift) + (key & (ps - 1));
           p = (lg << a.bt.page_shift) + (key & (ps - 1));
         };
@@ -454,8 +462,9 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
       if (work) {
         if ((flags & (kPgFirst | kPgOwner)) == (kPgFirst | kPgOwner)) {
           const int on = static_cast<int>(static_cast<unsigned>(pair + kPgPairCost + nt - 1) / static_cast<unsigned>(run));
-          a.cut[static_cast<long long>(b) * a.bt.Hkv + h] =
-              on == 0 ? make_int2(-1, -1) : make_int2(static_cast<int>(u), static_cast<int>(u) + on);
+          if (RA_IN_BOUNDS(b, a.bt.B) && RA_IN_BOUNDS(h, a.bt.Hkv) && RA_IN_BOUNDS(u + on, U))
+            a.cut[static_cast<long long>(b) * a.bt.Hkv + h] =
+                on == 0 ? make_int2(-1, -1) : make_int2(static_cast<int>(u), static_cast<int>(u) + on);
         }
         first = flags & kPgLast;
         ++t;
@@ -661,7 +670,8 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
       for (int nb = 0; nb < NB; ++nb) {
         qmax[nb] = 0u;
         const int r = row0 + 8 * nb + gr, tk = r / a.groups;
-        const bool real = r < a.rows && tk < fresh;
+        const bool real = r < a.rows && tk < fresh && RA_IN_BOUNDS(tk, a.bt.T) && RA_IN_BOUNDS(tile.b, a.bt.B) &&
+                          RA_IN_BOUNDS(tile.h, a.bt.Hkv);
         const __nv_bfloat16* qr =
             a.q + (real ? ((static_cast<long long>(tile.b) * a.bt.T + tk) * a.Hq + tile.h * a.groups + r % a.groups) * D : 0);
 #pragma unroll
@@ -1035,6 +1045,7 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
         if (flags & kPgWhole) {
           const long long row =
               (static_cast<long long>(tile.b) * a.bt.T + r / a.groups) * a.Hq + tile.h * a.groups + r % a.groups;
+          if (!RA_IN_BOUNDS(row, static_cast<long long>(a.bt.B) * a.bt.T * a.Hq)) continue;
           const float inv = has ? 1.f / l[i] : 0.f;
 #pragma unroll
           for (int c = 0; c < KS; ++c) {
@@ -1049,6 +1060,7 @@ __global__ void __launch_bounds__(PgSmem<D, ET, NB, TEAMS>::kThreads, 1)
           if (gr == 0) a.lse[row] = has ? (E[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
         } else {
           const long long pr = (2 * u + (flags & kPgOwner ? 1 : 0)) * a.rows + r;
+          if (!RA_IN_BOUNDS(pr, static_cast<long long>(gridDim.x) * teams * 2 * a.rows)) continue;
           float* dst = a.part_o + pr * D;
 #pragma unroll
           for (int c = 0; c < KS; ++c) {
@@ -1104,7 +1116,7 @@ __global__ void __launch_bounds__(32 * NW) paged_combine_kernel(const __grid_con
       ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int e = 0; e < kPer; ++e) v[k][e] = 0.f;
-      if (t <= cut.y) {
+      if (t <= cut.y && RA_IN_BOUNDS(part(t), 2LL * max_teams * a.rows)) {
         ml[k] = a.part_ml[part(t)];
         const float* src = a.part_o + part(t) * D + col;
 #pragma unroll
@@ -1161,6 +1173,7 @@ __global__ void __launch_bounds__(32 * NW) paged_combine_kernel(const __grid_con
   const float inv = has ? 1.f / L : 0.f;
   const int b = static_cast<int>(pair / a.bt.Hkv), h = static_cast<int>(pair % a.bt.Hkv);
   const long long row = (static_cast<long long>(b) * a.bt.T + r / a.groups) * a.Hq + h * a.groups + r % a.groups;
+  if (!RA_IN_BOUNDS(row, static_cast<long long>(a.bt.B) * a.bt.T * a.Hq)) return;
   if constexpr (kPer == 1)
     pg_store1(a, row, D, col, has ? acc[0] * inv : 0.f);
   else

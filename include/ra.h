@@ -515,8 +515,9 @@ const char* ra_version(void);
 /*
  * The checked build.  libra_b200_debug.so is this library compiled with
  * -DRA_DEBUG_BOUNDS: before every run-time-indexed global access (the rows
- * and heads of TMA copies, output rows, lse and Delta entries, merge rows) and
- * every segment-table read, the kernels check the index against the extent it
+ * and heads of TMA copies, output rows, lse and Delta entries, merge rows, the
+ * paged cache's table and list entries, cached rows, partial results and slots)
+ * and every segment-table read, the kernels check the index against the extent it
  * must lie in.  A failed check records RA_ERR_DEVICE_BOUNDS in the device
  * status word (ra_get_device_status), skips the access and ends the CTA's work;
  * nothing traps.  Not part of the method on the pages: a debugging aid.
