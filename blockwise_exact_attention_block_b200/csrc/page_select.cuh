@@ -109,11 +109,8 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_
           reinterpret_cast<const uint4*>(a.bounds + (static_cast<long long>(max(page, 0)) * a.bt.Hkv + h) * 2 * D) + qd;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-        if (page >= 0) {
-          x = src[4 * j];
-          y = src[D / 8 + 4 * j];
-        }
+        uint4 x = src[4 * j], y = src[D / 8 + 4 * j];
+        if (page < 0) x = y = make_uint4(0u, 0u, 0u, 0u);
         lo[i][j][0] = x.x, lo[i][j][1] = x.y, lo[i][j][2] = x.z, lo[i][j][3] = x.w;
         hi[i][j][0] = y.x, hi[i][j][1] = y.y, hi[i][j][2] = y.z, hi[i][j][3] = y.w;
       }
