@@ -178,3 +178,66 @@ def test_tiny_values_do_not_overflow_the_sum(cuda_lib, dtype, rows, shift, growt
         tol = 2.0 ** -15 + 2 * (each + sums) + 6 * 2.0 ** -23 + 2.0 ** -22
         assert off <= tol, f"off by {off:.3g}, {off / tol:.3g} tolerances"
     assert ra.ra_get_device_status() == ra.RA_OK
+
+
+def cut(x, bits):
+    """x (positive) cut off to its leading bits."""
+    e = np.floor(np.log2(x)) - (bits - 1)
+    return np.floor(x / 2.0 ** e) * 2.0 ** e
+
+
+def nearest(x, bits):
+    e = np.floor(np.log2(np.maximum(x, 1e-300))) - (bits - 1)
+    return np.rint(x / 2.0 ** e) * 2.0 ** e
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [1, 8, 12, 16, 32, 64])
+@pytest.mark.parametrize("n,D", [(32, 64), (100, 128)])
+def test_every_term_of_the_weights_is_there(cuda_lib, dtype, rows, n, D):
+    """One key with weight 1 and value 0, the others with one weight w and value 1: out =
+    (n - 1) w / (1 + (n - 1) w) shows w itself.  Each row's w is one that the leading bits
+    alone (and, in bf16, two terms) hold as badly as they can; the bound lies below half of
+    what either would be off.
+
+    The bound: x = log2 w goes through three roundings (2^-24 of it), the exponential has
+    2^-22, both scales' products 2^-24 each; they enter out and 1 + (n - 1) w alike, so out
+    takes no more than their part.  Then the terms' own loss (2^-24, 2^-22 for f16), 6 products
+    that may cut (2^-23), at most four parts and (100 / 32 + 7) sums in fp32, the
+    division and the output: 20 roundings of 2^-24."""
+    ra = cuda_lib
+    big = 4.6 if n > 64 else 3.4  # (n - 1) w about 1
+    grid = torch.arange(0.8 * big, 1.2 * big, 1 / 64).mul(math.sqrt(D)).to(torch.bfloat16).double().unique()
+    a = grid.numpy() / math.sqrt(D)
+    w = np.exp(-a)
+    bits = 8 if dtype == "bf16" else 11
+    one = cut(w, bits)
+    two = one + nearest(w - one, 8)
+    lost = np.abs(two - w) if dtype == "bf16" else np.abs(one - w)
+    pick = np.sort(np.argsort(-lost / w)[:rows] if rows <= len(w) // 3 else np.argsort(-lost / w)[:len(w) // 3])
+    pick = np.resize(pick, rows)
+    k, v = torch.zeros((n, D)), torch.ones((n, D))
+    k[1:, 0], k[:, 1] = -1.0, 1.0
+    v[0] = 0.0
+    v[0, 5] = 1.0
+    c = Shared(ra, dtype, k, v, 2, ps=16)
+    q = torch.zeros((2, 1, rows, D), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = grid[torch.tensor(pick)].to(torch.bfloat16).cuda()
+    out, _ = c.decode(ra, q, out_dtype=torch.float32)
+    out = out[:, 0].cpu().double().numpy()
+    kk, vv = c.k.cpu().numpy(), c.v.cpu().numpy()
+    assert np.array_equal(kk[1:, 0], -np.ones(n - 1)) and np.abs(vv[1:, 0] - 1).max() < 2.0 ** -23
+    W = w[pick]
+    want = (n - 1) * W / (1 + (n - 1) * W)
+    tol = want * (np.log2(1 / W) * 3 * 2.0 ** -24 * math.log(2) + 2.0 ** -22 + 2 * 2.0 ** -24
+                  + (2.0 ** -24 if dtype == "bf16" else 2.0 ** -22) + 6 * 2.0 ** -23 + 20 * 2.0 ** -24)
+    off = np.abs(out[..., 0] - want)
+    assert (off <= tol).all(), f"off by {(off / tol).max():.3g} tolerances"
+    for terms in (one, two) if dtype == "bf16" else (one,):
+        wrong = np.abs((n - 1) * terms[pick] / (1 + (n - 1) * W) - want)
+        assert np.median(wrong / tol) > 2, "the bound does not tell"
+    if dtype == "bf16":  # a bf16 output: its rounding, and two terms (2^-16)
+        got = c.decode(ra, q, out_dtype=torch.bfloat16)[0][:, 0, :, 0].cpu().double().numpy()
+        half = 2.0 ** -8 * want + tol + 2.0 ** -16 * want
+        assert (np.abs(got - want) <= half).all()
+    assert ra.ra_get_device_status() == ra.RA_OK
