@@ -323,7 +323,8 @@ int ra_decode_splits(int B, int Tq, int Skv, int Hq, int Hkv, int D, int n_split
  *             {64, 128}; n_pages * Hkv * page_size < 2^31 - 128.
  *  page_table  device int32 [B, max_pages]: page of tokens [i page_size,
  *             (i + 1) page_size) of a sequence.  Entries behind a sequence's
- *             last token are not read.
+ *             last token may hold anything and are not used (a call may load
+ *             them).
  *  B, max_pages  sequences; table entries of each (max_pages * page_size <= 2^31 - 256).
  *  seq_lens   device int32 [B]: tokens of each sequence in the cache, the new
  *             ones of this step included; 0 for an empty slot.
