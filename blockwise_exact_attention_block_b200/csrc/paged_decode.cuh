@@ -388,8 +388,16 @@ __device__ __forceinline__ void pg_walk(const PagedArgs& a, uint8_t* smem, volat
     if (x == -1) return -1;
     bool good = x >= 0 && x < pages;
     if (good) {
-      for (int i = idx - 2; (prev < 0 || prev >= pages) && i >= 0; --i) prev = sel[i];
-      good = x > prev || prev >= pages;
+      if (prev >= pages) prev = -1;
+      for (int i = idx - 2; prev < 0 && i >= 0; i -= 8) {  // over a gap, eight loads at a time
+        int y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = i >= e ? sel[i - e] : -1;
+#pragma unroll
+        for (int e = 7; e >= 0; --e)
+          if (y[e] >= 0 && y[e] < pages) prev = y[e];
+      }
+      good = x > prev;
     }
     if (!good) set_status(RA_ERR_DEVICE_BOUNDS);
     return good ? x : -1;
