@@ -12,8 +12,9 @@
 // sum: it is that of the sums in 64 bits, where products of bf16 values (16
 // bits) and their sums are exact unless the terms' exponents differ by more
 // than 30.  But 64-bit sums of every page cost more than reading the bounds
-// (25 us where this form takes 5: eight sequences of 2k to 24k keys, pages of
-// 16, 8 heads, 4 rows), and few pages are close to the border.  So: scores of all
+// (25 us by themselves, where scores and selection take 17.5 together: eight
+// sequences of 2k to 24k keys, pages of 16, 8 heads, 4 rows), and few pages are
+// close to the border.  So: scores of all
 // pages from the tensor core in fp32 with a bound on their error; the n_sel-th
 // largest of them; and 64-bit sums for the pages within the error of it.
 #pragma once

@@ -37,13 +37,16 @@
 // costs 5 to 7 % where instruction issue is the bound (8 x 9k-24k int8 keys, 16 rows:
 // 77.5 us then, 82 now), up to 13 % for a bf16 team of several warps, nothing where HBM is.
 //
-// Bound by HBM: a cached element meets the groups * Tq (<= 64) query rows of its
-// KV head and is used once.  So the cache is streamed once, through rings of
-// shared memory, by 16-byte asynchronous copies: a page of one head may be as
-// small as 1 KB and the tile's scales are 128 bytes, and a TMA copy costs the
-// same to issue whatever its size (with TMA, 16-key pages of int8 took 111 us
-// where 64-key ones took 88; eight sequences of 9k to 24k keys, 8 heads, 128
-// columns).  The products are mma.sync m16n8k16 with the keys
+// What bounds it: a cached element meets the groups * Tq (<= 64) query rows of its KV
+// head and is used once, so HBM bounds bf16 caches up to 16 rows (1M keys 174 us, 94 % of
+// the copy rate); instruction issue and its latency bound 8-bit ones (eight sequences of
+// 9k to 24k int8 keys, 8 heads, 128 columns: 58 us for 4 rows, 766 instructions a tile, 82
+// for 16 rows, 1,040 a tile at 40 % of the issue slots; HBM alone 42) and teams of several
+// warps (32 rows 191, of a bf16 cache 229).  So the cache is streamed once, through
+// rings of shared memory, by 16-byte asynchronous copies: a page of one head may be
+// as small as 1 KB and the tile's scales are 128 bytes, and a TMA copy costs the
+// same to issue whatever its size (with TMA, one token a sequence, 16-key pages of
+// those took 97 us where 64-key ones took 75).  The products are mma.sync m16n8k16 with the keys
 // (scores) or the columns (output) on the 16 side and the query rows on the 8
 // side: up to 8 rows, the usual single token, cost half of what rows on the 16
 // side would, in products, in exponentials and in accumulator registers.
